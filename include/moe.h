@@ -276,6 +276,114 @@ moe_status moe_grouped_swiglu(const MoEConfig *cfg, int rows, const void *x_perm
                               const float *row_weight, void *y_perm, void *ws, size_t ws_bytes,
                               moe_stream_t stream);
 
+/* ------------------------------------------------- products grouped by expert
+ *
+ * The products behind the layer, one by one and with their gradients, for
+ * training an expert FFN and for running it with both operands in 4 bits:
+ *
+ *   forward   gu = x_perm [W_gate; W_up]^T   moe_grouped_matmul (w [E, 2F, D])
+ *             h  = SwiGLU(gu)                moe_swiglu
+ *             y  = w_r (h W_down^T)          moe_grouped_matmul (w [E, D, F], row_weight)
+ *   backward  d  = dy W_down                 moe_grouped_matmul (transposed)
+ *             dgu, hw, dw_r                  moe_swiglu_backward
+ *             dW_down = dy^T hw              moe_grouped_wgrad
+ *             dx_perm = dgu [W_gate; W_up]   moe_grouped_matmul (transposed)
+ *             d[W_gate; W_up] = dgu^T x_perm moe_grouped_wgrad
+ *   4 bits    moe_quantize_nvfp4 (with the dispatch's row map), moe_grouped_matmul_nvfp4,
+ *             moe_swiglu_quantize_nvfp4, moe_grouped_matmul_nvfp4, then moe_combine on
+ *             the fp32 rows.
+ *
+ * Group e owns the rows expert_offsets[e] .. expert_offsets[e+1] - 1 (device
+ * int32 [groups + 1], not decreasing, as moe_dispatch writes it; NULL = one
+ * group of all rows, groups = 1).  Offsets are kept within [0, rows] before
+ * use.  A group may be empty.  Output rows before the first and from the last
+ * offset on are left as they were.  Sums are accumulated in fp32. */
+typedef struct {
+  int groups;          /* E, 1..1024 */
+  int rows;            /* rows of the token matrices; bounds every offset */
+  int n;               /* output columns (wgrad: columns of dy), a multiple of 8 */
+  int k;               /* reduction length (wgrad: columns of a), a multiple of 8; NVFP4: of 32 */
+  moe_dtype dtype;     /* operands: MOE_F32 (CUDA cores), MOE_BF16, MOE_NVFP4 (tensor cores) */
+  moe_dtype out_dtype; /* MOE_F32, or MOE_BF16 (not from F32 operands): one rounding of the fp32 result */
+} MoEGrouped;
+
+/* Bytes of workspace the three products below need (their device status
+ * word); 0 for sizes they refuse. */
+size_t moe_grouped_workspace_size(const MoEGrouped *g);
+
+/* y[r, :] = row_weight[r] * (a[r, :] W[e]^T)   w [E, n, k], transposed = 0
+ * y[r, :] = row_weight[r] * (a[r, :] W[e])     w [E, k, n], transposed = 1: the
+ *           gradient with respect to the input of a product stored as [E, k, n]
+ *   a [rows, k], y [rows, n] out_dtype, row_weight [rows] float or NULL (= 1) */
+moe_status moe_grouped_matmul(const MoEGrouped *g, const void *a, const int32_t *expert_offsets, const void *w,
+                              int transposed, const float *row_weight, void *y, void *ws, size_t ws_bytes,
+                              moe_stream_t stream);
+
+/* dw[e] = sum over the rows r of group e of dy[r, :]^T a[r, :]
+ *   dy [rows, n], a [rows, k], dw [E, n, k] out_dtype
+ * An empty group's dw is zero.  accumulate != 0: the sum is added to dw (in
+ * fp32, rounded once) and an empty group's dw is left as it is.  Each element
+ * is one sum in row order: deterministic. */
+moe_status moe_grouped_wgrad(const MoEGrouped *g, const void *dy, const void *a, const int32_t *expert_offsets,
+                             int accumulate, void *dw, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The product of two NVFP4 operands (layout as in MoEWeights: two codes per
+ * byte, an e4m3 scale per 16), each with optional fp32 row scales:
+ *   y[r, n] = row_weight[r] * a_row_scale[r] * w_row_scale[e, n] * sum_k A[r, k] W[e, n, k]
+ *   a uint8 [rows, k/2], a_scales [rows, k/16], a_row_scale [rows] or NULL (= 1)
+ *   w uint8 [E, n, k/2], w_scales [E, n, k/16], w_row_scale [E, n] or NULL
+ *   row_weight [rows] or NULL; y [rows, n] out_dtype; g->dtype = MOE_NVFP4
+ * Codes times scales are multiplied exactly and accumulated in fp32. */
+moe_status moe_grouped_matmul_nvfp4(const MoEGrouped *g, const void *a, const void *a_scales, const float *a_row_scale,
+                                    const int32_t *expert_offsets, const void *w, const void *w_scales,
+                                    const float *w_row_scale, const float *row_weight, void *y, void *ws,
+                                    size_t ws_bytes, moe_stream_t stream);
+
+/* Quantises rows to NVFP4:
+ *   row scale  rs = 2^ceil(log2(max|row| / 2688)), at least 2^-110 (row_scale [rows] out;
+ *              NULL: rs = 1, the format of MoEWeights, where block maxima below
+ *              6 * 2^-10 become zero)
+ *   scale      s = e4m3(max|block| / (6 rs)) per 16 elements, to nearest even, at most 448
+ *   code       q = e2m1(x / (s rs)), to nearest even, at most 6 in magnitude; 0 where s = 0
+ * so an element stands for q * s * rs.  A block with an infinity or a NaN gets
+ * the NaN scale (0x7f) and codes 0, and takes no part in the row's scale.
+ *   x         [x_rows, cols] dtype (MOE_F32 or MOE_BF16); cols a multiple of 16
+ *   row_token [rows] or NULL: row r is quantised from x[row_token[r]] (the dispatch's
+ *             gather); a row whose index is outside x is left as it was.  NULL:
+ *             from x[r], and x_rows >= rows
+ *   live_rows device int32 or NULL: only rows below *live_rows are written
+ *             (expert_offsets + E after a dispatch)
+ *   codes uint8 [rows, cols/2], scales uint8 [rows, cols/16], row_scale above
+ *   values    bf16 [rows, cols] or NULL: what the codes stand for (exact in bf16; infinite
+ *             where that is beyond bf16's range) */
+moe_status moe_quantize_nvfp4(int rows, int cols, moe_dtype dtype, const void *x, int x_rows, const int32_t *row_token,
+                              const int32_t *live_rows, void *codes, void *scales, float *row_scale, void *values,
+                              moe_stream_t stream);
+
+/* moe_swiglu and moe_quantize_nvfp4 of its result (rounded to dtype) in one
+ * pass: gu [rows, 2 cols] as in moe_swiglu, the outputs as above.  The same
+ * bits as the two calls. */
+moe_status moe_swiglu_quantize_nvfp4(int rows, int cols, moe_dtype dtype, const void *gu, float clamp,
+                                     moe_clamp_mode clamp_mode, const int32_t *live_rows, void *codes, void *scales,
+                                     float *row_scale, void *values, moe_stream_t stream);
+
+/* h[r, :] = SiLU(clip(g)) * clip(u), gu [rows, 2F] = (g | u), h [rows, F], both
+ * dtype (MOE_F32 or MOE_BF16); F a multiple of 8; clamp 0 = no clip, modes as in
+ * MoEConfig.  live_rows as above.  A NaN stays one through the clip. */
+moe_status moe_swiglu(int rows, int F, moe_dtype dtype, const void *gu, float clamp, moe_clamp_mode clamp_mode,
+                      const int32_t *live_rows, void *h, moe_stream_t stream);
+
+/* Backward of y[r] = row_weight[r] * (h[r] W_down^T) down to gate|up, given
+ * dh = dy W_down (not multiplied by row_weight):
+ *   dgu          [rows, 2F]: gradient of gu, row_weight included (may be gu itself)
+ *   hw           [rows, F] or NULL: row_weight[r] * h[r], the operand of dW_down = dy^T hw
+ *   drow_weight  [rows] float or NULL: sum over F of dh * h
+ * row_weight [rows] or NULL (= 1).  A clipped g or u gets no gradient, nor does
+ * anything behind a clipped h (MOE_CLAMP_OUTPUT).  Deterministic. */
+moe_status moe_swiglu_backward(int rows, int F, moe_dtype dtype, const void *gu, const void *dh,
+                               const float *row_weight, float clamp, moe_clamp_mode clamp_mode,
+                               const int32_t *live_rows, void *dgu, void *hw, float *drow_weight, moe_stream_t stream);
+
 /* ---------------------------------------------------------- stage 4: combine */
 
 /* out[t, :] = sum_{j=0..k-1, slot_row[t,j] >= 0} y_perm[slot_row[t, j], :]

@@ -7,6 +7,7 @@ no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from ctypes import POINTER, c_char_p, c_float, c_int, c_size_t, c_uint64, c_void_p
@@ -43,6 +44,10 @@ class MoEWeights(ctypes.Structure):
                                         "s_down", "sh_gate", "sh_up", "sh_down", "bias", "bias_vl")]
 
 
+class MoEGrouped(ctypes.Structure):
+    _fields_ = [("groups", c_int), ("rows", c_int), ("n", c_int), ("k", c_int), ("dtype", c_int), ("out_dtype", c_int)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -56,7 +61,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                           "`python -m mixture_experts_layer_sqrt_b200.build` (nvcc, sm_100a)")
     lib = ctypes.CDLL(path)
     P, I, S = c_void_p, c_int, c_size_t
-    cfgp, wp = POINTER(MoEConfig), POINTER(MoEWeights)
+    cfgp, wp, gp, F = POINTER(MoEConfig), POINTER(MoEWeights), POINTER(MoEGrouped), c_float
     sig = {
         "moe_status_string": (c_char_p, [I]),
         "moe_version": (c_char_p, []),
@@ -80,6 +85,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_forward": (I, [cfgp, I, P, wp, P, P, P, P, P, S, P]),
         "moe_forward_profiled": (I, [cfgp, I, P, wp, P, P, P, P, P, S, P, P, I]),
         "moe_selftest_wait_timeout": (I, [P, S, P]),
+        "moe_grouped_workspace_size": (S, [gp]),
+        "moe_grouped_matmul": (I, [gp, P, P, P, I, P, P, P, S, P]),
+        "moe_grouped_wgrad": (I, [gp, P, P, P, I, P, P, S, P]),
+        "moe_grouped_matmul_nvfp4": (I, [gp, P, P, P, P, P, P, P, P, P, P, S, P]),
+        "moe_quantize_nvfp4": (I, [I, I, I, P, I, P, P, P, P, P, P, P]),
+        "moe_swiglu_quantize_nvfp4": (I, [I, I, I, P, F, I, P, P, P, P, P, P]),
+        "moe_swiglu": (I, [I, I, I, P, F, I, P, P, P]),
+        "moe_swiglu_backward": (I, [I, I, I, P, P, P, F, I, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -96,7 +109,9 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_expert_capacity", "moe_launc
            "moe_check_device_status", "moe_route_workspace_size", "moe_route_topk", "moe_dispatch_workspace_size",
            "moe_dispatch", "moe_dispatch_noalloc", "moe_grouped_swiglu_workspace_size", "moe_expert_workspace_size",
            "moe_expert_gate_up", "moe_expert_down", "moe_grouped_swiglu", "moe_combine",
-           "moe_workspace_size", "moe_forward", "moe_forward_profiled", "moe_selftest_wait_timeout")
+           "moe_workspace_size", "moe_forward", "moe_forward_profiled", "moe_selftest_wait_timeout",
+           "moe_grouped_workspace_size", "moe_grouped_matmul", "moe_grouped_wgrad", "moe_grouped_matmul_nvfp4",
+           "moe_quantize_nvfp4", "moe_swiglu_quantize_nvfp4", "moe_swiglu", "moe_swiglu_backward")
 
 
 def status_string(s: int) -> str:
@@ -304,6 +319,255 @@ def forward(cfg: MoEConfig, x: torch.Tensor, w: MoEWeights, ws: torch.Tensor, im
                            _p(topk_idx_out), _p(expert_counts_out), _p(ws), ws.numel(), _stream(stream)),
            "moe_forward")
     return out
+
+
+# ------------------------------------------------------------------ products grouped by expert
+
+_TORCH_OUT = {"f32": torch.float32, "bf16": torch.bfloat16}
+_DTYPE_OF = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _on(stream, first: torch.Tensor, *others: Optional[torch.Tensor]):
+    """The context to allocate and launch in: the device of the tensors (all on one)
+    and `stream`, so that what is allocated for the call belongs to the stream that uses it."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got one on {dev}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return contextlib.nullcontext()
+
+
+def _act_dtype(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in _DTYPE_OF:
+        raise ValueError(f"{what}: expected float32 or bfloat16, got {t.dtype}")
+    return _DTYPE_OF[t.dtype]
+
+
+def _need(t: torch.Tensor, shape, dtype, what: str) -> None:
+    if t is None:
+        raise ValueError(f"{what} is missing")
+    _expect(t, shape, dtype, what)
+
+
+def _matrix(t: torch.Tensor, dims: int, what: str) -> None:
+    if t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor of {dims} dimensions, got {tuple(t.shape)}")
+
+
+def _groups(offsets: Optional[torch.Tensor], E: int) -> None:
+    if offsets is None:
+        if E != 1:
+            raise ValueError("offsets may be left out for one group only")
+        return
+    _expect(offsets, (E + 1,), torch.int32, "offsets")
+
+
+def grouped_workspace_size(E: int, N: int, K: int, rows: int, dtype: str = "bf16", out: Optional[str] = None) -> int:
+    g = MoEGrouped(E, rows, N, K, DTYPES[dtype], DTYPES[out or ("f32" if dtype == "f32" else "bf16")])
+    return int(lib.moe_grouped_workspace_size(ctypes.byref(g)))
+
+
+def grouped_matmul(a: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Tensor], transposed: bool = False,
+                   row_weight: Optional[torch.Tensor] = None, y=None, out: Optional[str] = None, ws=None,
+                   stream=None) -> torch.Tensor:
+    """Rows of group e times w[e]: y = a w[e]^T with w [E, N, K], or y = a w[e] with w [E, K, N]
+    when transposed (the input gradient of a product stored as [E, K, N]).  `out`: "bf16" or
+    "f32" (by default the type of y, or of a)."""
+    _matrix(a, 2, "a")
+    _matrix(w, 3, "w")
+    rows, K = a.shape
+    E = w.shape[0]
+    N = w.shape[2] if transposed else w.shape[1]
+    _need(w, (E, K, N) if transposed else (E, N, K), a.dtype, "w")
+    _groups(offsets, E)
+    _expect(row_weight, (rows,), torch.float32, "row_weight")
+    odt = _TORCH_OUT[out] if out else (y.dtype if y is not None else a.dtype)
+    g = MoEGrouped(E, rows, N, K, _act_dtype(a, "a"), _DTYPE_OF.get(odt, -1))
+    _expect(y, (rows, N), odt, "y")
+    with _on(stream, a, w, offsets, row_weight, y, ws):
+        if y is None:
+            y = torch.empty((rows, N), dtype=odt, device=a.device)
+        if ws is None:
+            ws = workspace(256, a.device)
+        _check(lib.moe_grouped_matmul(ctypes.byref(g), _p(a), _p(offsets), _p(w), int(transposed), _p(row_weight),
+                                      _p(y), _p(ws), ws.numel(), _stream()), "moe_grouped_matmul")
+    return y
+
+
+def grouped_wgrad(dy: torch.Tensor, a: torch.Tensor, offsets: Optional[torch.Tensor], dw=None, accumulate: bool = False,
+                  out: Optional[str] = None, ws=None, stream=None) -> torch.Tensor:
+    """dw[e] = dy_e^T a_e over the rows of group e, [E, N, K]; accumulate adds to the given dw."""
+    _matrix(dy, 2, "dy")
+    _matrix(a, 2, "a")
+    rows, N = dy.shape
+    K = a.shape[1]
+    _need(a, (rows, K), dy.dtype, "a")
+    if offsets is None:
+        E = 1
+    else:
+        E = offsets.numel() - 1
+        _groups(offsets, E)
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+    odt = _TORCH_OUT[out] if out else (dw.dtype if dw is not None else a.dtype)
+    g = MoEGrouped(E, rows, N, K, _act_dtype(a, "a"), _DTYPE_OF.get(odt, -1))
+    _expect(dw, (E, N, K), odt, "dw")
+    with _on(stream, a, dy, offsets, dw, ws):
+        if dw is None:
+            dw = torch.empty((E, N, K), dtype=odt, device=a.device)
+        if ws is None:
+            ws = workspace(256, a.device)
+        _check(lib.moe_grouped_wgrad(ctypes.byref(g), _p(dy), _p(a), _p(offsets), int(accumulate), _p(dw), _p(ws),
+                                     ws.numel(), _stream()), "moe_grouped_wgrad")
+    return dw
+
+
+def grouped_matmul_nvfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                         offsets: Optional[torch.Tensor], a_row_scale=None, w_row_scale=None, row_weight=None, y=None,
+                         out: Optional[str] = None, ws=None, stream=None) -> torch.Tensor:
+    """Rows of group e times w[e]^T, both NVFP4: a uint8 [rows, K/2] with a_scales [rows, K/16],
+    w uint8 [E, N, K/2] with w_scales [E, N, K/16], optional fp32 row scales of either."""
+    _matrix(a, 2, "a")
+    _matrix(w, 3, "w")
+    rows, K = a.shape[0], 2 * a.shape[1]
+    E, N = w.shape[:2]
+    _need(a, (rows, K // 2), torch.uint8, "a")
+    _need(w, (E, N, K // 2), torch.uint8, "w")
+    _need(a_scales, (rows, K // 16), torch.uint8, "a_scales")
+    _need(w_scales, (E, N, K // 16), torch.uint8, "w_scales")
+    _groups(offsets, E)
+    _expect(a_row_scale, (rows,), torch.float32, "a_row_scale")
+    _expect(w_row_scale, (E, N), torch.float32, "w_row_scale")
+    _expect(row_weight, (rows,), torch.float32, "row_weight")
+    odt = _TORCH_OUT[out] if out else (y.dtype if y is not None else torch.bfloat16)
+    g = MoEGrouped(E, rows, N, K, MOE_NVFP4, _DTYPE_OF.get(odt, -1))
+    _expect(y, (rows, N), odt, "y")
+    with _on(stream, a, a_scales, w, w_scales, offsets, a_row_scale, w_row_scale, row_weight, y, ws):
+        if y is None:
+            y = torch.empty((rows, N), dtype=odt, device=a.device)
+        if ws is None:
+            ws = workspace(256, a.device)
+        _check(lib.moe_grouped_matmul_nvfp4(ctypes.byref(g), _p(a), _p(a_scales), _p(a_row_scale), _p(offsets), _p(w),
+                                            _p(w_scales), _p(w_row_scale), _p(row_weight), _p(y), _p(ws), ws.numel(),
+                                            _stream()), "moe_grouped_matmul_nvfp4")
+    return y
+
+
+def _live(offsets: Optional[torch.Tensor]):
+    """Device address of the offsets' last entry, the number of rows in use."""
+    if offsets is None:
+        return None
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.numel() < 1:
+        raise ValueError("offsets: expected a contiguous int32 vector")
+    return offsets.data_ptr() + 4 * (offsets.numel() - 1)
+
+
+def _nvfp4_outputs(rows: int, cols: int, dev, row_scaled: bool, values: bool, out) -> Dict[str, torch.Tensor]:
+    shapes = dict(codes=((rows, cols // 2), torch.uint8), scales=((rows, cols // 16), torch.uint8),
+                  row_scale=((rows,), torch.float32) if row_scaled else None,
+                  values=((rows, cols), torch.bfloat16) if values else None)
+    if out is None:
+        return {k: None if s is None else torch.empty(s[0], dtype=s[1], device=dev) for k, s in shapes.items()}
+    for k, s in shapes.items():
+        if s is None:
+            if out.get(k) is not None:
+                raise ValueError(f"out has {k}, which this call does not write")
+            continue
+        _need(out.get(k), s[0], s[1], k)
+    return {k: out.get(k) for k in shapes}
+
+
+def quantize_nvfp4(x: torch.Tensor, row_token: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+                   row_scaled: bool = True, values: bool = False, out: Optional[Dict[str, torch.Tensor]] = None,
+                   stream=None) -> Dict[str, Optional[torch.Tensor]]:
+    """NVFP4 of the rows of x, or of x[row_token]: codes [rows, cols/2], scales [rows, cols/16],
+    row_scale [rows] (None with row_scaled=False: the format of the layer's weights) and, on
+    request, the bf16 values the codes stand for.  With offsets only the rows below its last
+    entry are written."""
+    _matrix(x, 2, "x")
+    x_rows, cols = x.shape
+    dt = _act_dtype(x, "x")
+    rows = x_rows
+    if row_token is not None:
+        rows = row_token.numel()
+        _expect(row_token, (rows,), torch.int32, "row_token")
+    o = out or {}
+    with _on(stream, x, row_token, offsets, *[t for t in o.values() if t is not None]):
+        o = _nvfp4_outputs(rows, cols, x.device, row_scaled, values, out)
+        _check(lib.moe_quantize_nvfp4(rows, cols, dt, _p(x), x_rows, _p(row_token), _live(offsets), _p(o["codes"]),
+                                      _p(o["scales"]), _p(o["row_scale"]), _p(o["values"]), _stream()),
+               "moe_quantize_nvfp4")
+    return o
+
+
+def _gate_up(gu: torch.Tensor):
+    _matrix(gu, 2, "gu")
+    if gu.shape[1] % 2:
+        raise ValueError("gu: expected gate and up columns side by side")
+    return gu.shape[0], gu.shape[1] // 2, _act_dtype(gu, "gu")
+
+
+def swiglu_quantize_nvfp4(gu: torch.Tensor, clamp: float = 0.0, clamp_mode="preact",
+                          offsets: Optional[torch.Tensor] = None, row_scaled: bool = True, values: bool = False,
+                          out: Optional[Dict[str, torch.Tensor]] = None,
+                          stream=None) -> Dict[str, Optional[torch.Tensor]]:
+    """quantize_nvfp4(swiglu(gu)) in one pass over gu [rows, 2 cols]."""
+    rows, cols, dt = _gate_up(gu)
+    o = out or {}
+    with _on(stream, gu, offsets, *[t for t in o.values() if t is not None]):
+        o = _nvfp4_outputs(rows, cols, gu.device, row_scaled, values, out)
+        _check(lib.moe_swiglu_quantize_nvfp4(rows, cols, dt, _p(gu), clamp, CLAMP_MODES[clamp_mode], _live(offsets),
+                                             _p(o["codes"]), _p(o["scales"]), _p(o["row_scale"]), _p(o["values"]),
+                                             _stream()), "moe_swiglu_quantize_nvfp4")
+    return o
+
+
+def swiglu(gu: torch.Tensor, clamp: float = 0.0, clamp_mode="preact", offsets: Optional[torch.Tensor] = None, h=None,
+           stream=None) -> torch.Tensor:
+    """h = SiLU(g) u of gu [rows, 2F] = (g | u).  With offsets only the rows below its last entry."""
+    rows, F, dt = _gate_up(gu)
+    _expect(h, (rows, F), gu.dtype, "h")
+    with _on(stream, gu, offsets, h):
+        if h is None:
+            h = torch.empty((rows, F), dtype=gu.dtype, device=gu.device)
+        _check(lib.moe_swiglu(rows, F, dt, _p(gu), clamp, CLAMP_MODES[clamp_mode], _live(offsets), _p(h), _stream()),
+               "moe_swiglu")
+    return h
+
+
+def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, row_weight: Optional[torch.Tensor] = None, clamp: float = 0.0,
+                    clamp_mode="preact", offsets: Optional[torch.Tensor] = None, need_hw: bool = True,
+                    need_drow_weight: bool = True, out: Optional[Dict[str, torch.Tensor]] = None,
+                    stream=None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients behind y = row_weight * (h W_down^T) from dh = dy W_down: dgu [rows, 2F], hw =
+    row_weight * h [rows, F] and drow_weight [rows] (either None when not needed).  out may hold
+    the tensors to write; out["dgu"] may be gu itself."""
+    rows, F, dt = _gate_up(gu)
+    _need(dh, (rows, F), gu.dtype, "dh")
+    _expect(row_weight, (rows,), torch.float32, "row_weight")
+    shapes = dict(dgu=((rows, 2 * F), gu.dtype), hw=((rows, F), gu.dtype) if need_hw else None,
+                  drow_weight=((rows,), torch.float32) if need_drow_weight else None)
+    o = out or {}
+    for k, s in shapes.items():
+        if o.get(k) is not None:
+            if s is None:
+                raise ValueError(f"out has {k}, which this call does not write")
+            _expect(o[k], s[0], s[1], k)
+    with _on(stream, gu, dh, row_weight, offsets, *[t for t in o.values() if t is not None]):
+        r = {k: o.get(k) if o.get(k) is not None or s is None else torch.empty(s[0], dtype=s[1], device=gu.device)
+             for k, s in shapes.items()}
+        _check(lib.moe_swiglu_backward(rows, F, dt, _p(gu), _p(dh), _p(row_weight), clamp, CLAMP_MODES[clamp_mode],
+                                       _live(offsets), _p(r["dgu"]), _p(r["hw"]), _p(r["drow_weight"]), _stream()),
+               "moe_swiglu_backward")
+    return r
 
 
 STAGES = ("route", "dispatch", "gate_up", "down", "shared", "combine")

@@ -246,7 +246,8 @@ int moe_checked_build(void) { return kChecked ? 1 : 0; }
 
 uint64_t moe_checked_violations(void) {
   return (uint64_t)violations_dispatch() + violations_combine() + violations_gemm_tc() + violations_gemm_fp4() +
-         violations_gemm_simt();
+         violations_gemm_simt() + violations_gemm_grouped() + violations_gemm_grouped_f32() +
+         violations_gemm_grouped_fp4() + violations_quantize();
 }
 
 moe_status moe_check_device_status(void *ws, moe_stream_t stream) {

@@ -1,0 +1,507 @@
+// Products grouped by expert with ragged group sizes, and their gradients, in
+// bf16 on the 5th-generation tensor cores (tcgen05 + TMEM + TMA), fp32
+// accumulation.  Group e owns the rows off[e] <= r < off[e+1] of A.
+//
+//   NT  y[r, :] = w_r * a[r, :] . W[e]^T        W [E, N, K]   (forward)
+//   NN  y[r, :] = w_r * a[r, :] . W[e]          W [E, K, N]   (input gradient of a
+//                                               product whose weights are [E, K, N])
+//   TN  dW[e] (+)= sum_{r in e} dy[r, :]^T a[r, :]            (weight gradient)
+//
+// NT and NN put the weights on the MMA's M side and the tokens on its N side:
+// a tile is 128 output features x up to BT tokens of one group, and its MMAs
+// run with N = the tile's tokens rounded up to 16.  A ragged group therefore
+// pads no MMA rows (with the tokens on the M side every group pads to 128),
+// weights are read once per BT tokens, and for a handful of tokens the MMA is
+// small and the kernel is a pure stream of the weights through the stage
+// ring.  TN puts dy's features on M, a's on N and reduces over the group's
+// rows; both operands are read as they lie (MN-major tiles), nothing is
+// transposed in memory.
+//
+// A K-major tile lies in shared memory as rows of 64 reduction elements (128
+// bytes, 128-byte swizzle); an MN-major tile as boxes of 64 features x 64
+// reduction elements, a 128-byte line per reduction element.  The last block
+// of a TN reduction brings in rows of the next group (or none): their lines
+// are set to zero in both operands before the MMAs read them, so that nothing
+// there, NaN included, reaches this group's sum.
+//
+// Roles (192 threads per CTA, persistent, one CTA per SM):
+//   warp 0    TMA producer into the stage ring
+//   warp 1    TMEM owner; one thread issues the MMAs (4 x K=16 per stage);
+//             two accumulators let the epilogue of tile i overlap the MMAs
+//             of tile i+1.  TN: the warp first clears the lines above.
+//   warps 2-5 epilogue: TMEM lane = output feature.
+//
+// Every wait is bounded (2 s, then MOE_ERR_DEVICE_TIMEOUT in the status word
+// and an orderly wind down).
+#include <cudaTypedefs.h>
+#include <limits.h>
+
+#include "grouped.cuh"
+#include "kernels.h"
+#include "tma_host.h"
+
+namespace moe {
+
+MOE_VIOLATION_COUNTER(violations_gemm_grouped)
+
+namespace {
+
+using namespace grouped;
+
+enum Mode { NT = 0, NN = 1, TN = 2 };
+
+constexpr int BM = 128;              // output features per tile (TMEM lanes)
+constexpr int BK = 64;               // reduction elements per stage
+constexpr int UMMA_K = 16;
+constexpr int A_BYTES = BM * BK * 2;  // 16 KB
+constexpr int BOX = 64 * BK * 2;     // 8 KB: an MN-major box
+constexpr int TOK_BOX = 32;          // token rows per TMA box (NT, NN)
+constexpr int kThreads = 192;
+
+// BT: tokens (NT, NN) or columns (TN) per tile, the MMA's largest N.
+template <int BT>
+struct Cfg {
+  static constexpr int B_BYTES = BT * BK * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = BT == 256 ? 4 : 8;
+  static constexpr uint32_t TMEM_COLS = 2 * BT;
+};
+
+template <int STAGES>
+struct Smem {
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t tmem_full[2];
+  uint64_t tmem_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int start[MAX_E + 1];
+};
+constexpr int kSmemPart = 4608;                 // barriers and tile list
+constexpr int kStaging = 4 * 32 * 32 * 4;       // TN epilogue: 4 KB per warp
+static_assert(sizeof(Smem<8>) <= kSmemPart, "the epilogue staging follows the barriers and tile list");
+
+struct Params {
+  int rows, N, K, E;
+  int m_blocks;    // 128-feature blocks of the output
+  int n_blocks;    // TN: BT-column blocks
+  const int32_t *offsets;
+  const float *row_weight;
+  void *out;       // y [rows, N] or dW [E, N, K]
+  int out_f32;
+  int accumulate;  // TN
+  int *status;
+};
+
+// Shared-memory descriptor of an MN-major tile with the 128-byte swizzle:
+// boxes of 64 features (128 bytes) x 64 reduction elements; leading byte
+// offset = next 64 features (one box), stride byte offset = next 8 reduction
+// elements (1024 bytes).
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(BOX >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+template <Mode MODE, int BT>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
+  using C = Cfg<BT>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *stage_a = base;
+  uint8_t *stage_b = base + STAGES * A_BYTES;
+  Smem<STAGES> &sm = *reinterpret_cast<Smem<STAGES> *>(base + STAGES * C::STAGE_BYTES);
+  uint32_t *staging = reinterpret_cast<uint32_t *>(base + STAGES * C::STAGE_BYTES + kSmemPart);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      ptx::mbar_init(&sm.full[s], 1);
+      ptx::mbar_init(&sm.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&sm.tmem_full[a], 1);
+      ptx::mbar_init(&sm.tmem_empty[a], 4);
+    }
+    ptx::mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&sm.tmem_base, C::TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  if (warp == 2) {
+    // TN needs no tile list (every group has m_blocks * n_blocks tiles), but
+    // the same check of the offsets
+    const bool ok = scan_tiles(p.offsets, p.rows, p.E, BT, sm.start);
+    if (kChecked && !ok && lane == 0 && blockIdx.x == 0) note_violation();
+    if (kChecked && MODE == TN && lane == 0) sm.start[0] = ok ? 0 : 1;
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = sm.tmem_base;
+  int total;
+  if (MODE == TN) total = (kChecked && sm.start[0]) ? 0 : p.E * p.m_blocks * p.n_blocks;
+  else total = sm.start[p.E] * p.m_blocks;
+
+  // tile t -> group, feature block, first row / column, reduction blocks
+  struct Tile {
+    int e, m0, c0, count, row0, red;  // c0: first column (TN); count: tokens or columns; red: reduction length
+  };
+  auto tile_of = [&](int t) {
+    Tile r;
+    if (MODE == TN) {
+      const int per = p.m_blocks * p.n_blocks;
+      r.e = t / per;
+      const int local = t - r.e * per;
+      const int nb = local / p.m_blocks;
+      r.m0 = (local - nb * p.m_blocks) * BM;
+      r.c0 = nb * BT;
+      r.count = p.K - r.c0 < BT ? p.K - r.c0 : BT;
+      r.row0 = seg_begin(p.offsets, p.rows, r.e);
+      r.red = seg_end(p.offsets, p.rows, r.e) - r.row0;
+      if (r.red < 0) r.red = 0;
+    } else {
+      const TokenTile tt = token_tile(sm.start, p.offsets, p.rows, p.E, p.m_blocks, t);
+      r.e = tt.e;
+      r.m0 = tt.blk * BM;
+      r.c0 = 0;
+      r.row0 = tt.row0;
+      r.count = tt.count;
+      r.red = p.K;
+    }
+    return r;
+  };
+
+  if (warp == 0) {
+    // ================================================= TMA producer
+    if (lane == 0) {
+      Ring<STAGES> ring;
+      uint32_t issued = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const Tile tl = tile_of(t);
+        const int kbs = (tl.red + BK - 1) / BK;
+        const int boxes = MODE == TN ? (tl.count + 63) / 64 : (tl.count + TOK_BOX - 1) / TOK_BOX;
+        const uint32_t tx = A_BYTES + (uint32_t)boxes * (MODE == TN ? BOX : TOK_BOX * BK * 2);
+        for (int kb = 0; kb < kbs; ++kb, ring.next(), ++issued) {
+          if (!wait_bar<true>(&sm.empty[ring.s], ring.ph ^ 1u, &sm.abort, p.status)) {
+            ok = false;
+            break;
+          }
+          uint64_t *bar = &sm.full[ring.s];
+          uint8_t *a = stage_a + ring.s * A_BYTES;
+          uint8_t *b = stage_b + ring.s * C::B_BYTES;
+          const int k0 = kb * BK;
+          ptx::mbar_arrive_expect_tx(bar, tx);
+          if (MODE == NT) {
+            ptx::tma_load_3d(a, &tmA, bar, k0, tl.m0, tl.e);
+          } else if (MODE == NN) {
+            ptx::tma_load_3d(a, &tmA, bar, tl.m0, k0, tl.e);
+            ptx::tma_load_3d(a + BOX, &tmA, bar, tl.m0 + 64, k0, tl.e);
+          } else {
+            ptx::tma_load_2d(a, &tmA, bar, tl.m0, tl.row0 + k0);
+            ptx::tma_load_2d(a + BOX, &tmA, bar, tl.m0 + 64, tl.row0 + k0);
+          }
+          for (int i = 0; i < boxes; ++i) {
+            if (MODE == TN) ptx::tma_load_2d(b + i * BOX, &tmB, bar, tl.c0 + i * 64, tl.row0 + k0);
+            else ptx::tma_load_2d(b + i * TOK_BOX * BK * 2, &tmB, bar, k0, tl.row0 + i * TOK_BOX);
+          }
+        }
+      }
+      // every issued copy has landed before shared memory is released
+      for (int s = 0; s < STAGES; ++s) {
+        if ((uint32_t)s >= issued) break;
+        const uint32_t last = (issued - 1 - s) / STAGES;  // this stage's last round
+        drain_bar(&sm.full[s], last & 1u, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ================================================= MMA issuer
+    // D fp32, A and B bf16; bit 15: A is MN-major, bit 16: B is
+    constexpr uint32_t idesc0 =
+        ptx::idesc_bf16_f32(BM, 0) | (MODE != NT ? 1u << 15 : 0u) | (MODE == TN ? 1u << 16 : 0u);
+    Ring<STAGES> ring;
+    int i = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const Tile tl = tile_of(t);
+      const int kbs = (tl.red + BK - 1) / BK;
+      if (kbs == 0) continue;  // TN, empty group: the epilogue needs no sum
+      const int acc = i & 1;
+      const uint32_t aph = (i >> 1) & 1u;
+      ++i;
+      if (!warp_wait<false>(&sm.tmem_empty[acc], aph ^ 1u, &sm.abort, p.status)) break;
+      ptx::tc_fence_after();
+      const uint32_t d_tmem = tmem_base + acc * BT;
+      const uint32_t idesc = idesc0 | (uint32_t)((tl.count + 15) >> 4) << 18;  // N >> 3 at bit 17, N a multiple of 16
+      for (int kb = 0; kb < kbs; ++kb, ring.next()) {
+        if (!warp_wait<true>(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) {
+          ok = false;
+          break;
+        }
+        uint8_t *a = stage_a + ring.s * A_BYTES;
+        uint8_t *b = stage_b + ring.s * C::B_BYTES;
+        const int left = tl.red - kb * BK;
+        int steps = BK / UMMA_K;
+        if (MODE == TN && left < BK) {
+          // lines [left, steps * 16) of every box belong to other rows
+          steps = (left + UMMA_K - 1) / UMMA_K;
+          const int lines = steps * UMMA_K - left;
+          __syncwarp();  // the copies that lane 0 saw land are ordered before every lane's stores
+          const int boxes = (tl.count + 63) / 64;
+          for (int j = lane; j < lines * 8 * (2 + boxes); j += 32) {
+            const int box = j / (lines * 8), in = j - box * lines * 8;
+            uint8_t *q = (box < 2 ? a + box * BOX : b + (box - 2) * BOX) + left * 128 + in * 16;
+            *reinterpret_cast<uint4 *>(q) = make_uint4(0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          ptx::tc_fence_after();
+          const uint32_t aa = ptx::smem_addr(a), ba = ptx::smem_addr(b);
+          for (int k = 0; k < steps; ++k) {
+            const uint64_t ad = MODE == NT ? ptx::desc_kmajor_sw128(aa + k * UMMA_K * 2)
+                                           : desc_mnmajor_sw128(aa + k * UMMA_K * 128);
+            const uint64_t bd = MODE == TN ? desc_mnmajor_sw128(ba + k * UMMA_K * 128)
+                                           : ptx::desc_kmajor_sw128(ba + k * UMMA_K * 2);
+            ptx::mma_bf16(d_tmem, ad, bd, idesc, (kb | k) != 0);
+          }
+          ptx::mma_commit(&sm.empty[ring.s]);
+        }
+        __syncwarp();
+      }
+      if (ok && lane == 0) ptx::mma_commit(&sm.tmem_full[acc]);
+      __syncwarp();
+    }
+    if (lane == 0) {  // all issued MMAs complete before TMEM is released
+      ptx::mma_commit(&sm.drain);
+      drain_bar(&sm.drain, 0, p.status);
+    }
+    __syncwarp();
+  } else {
+    // ================================================= epilogue (warps 2..5)
+    const int q = warp & 3;  // TMEM lane quadrant this warp may access
+    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    int i = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+      const Tile tl = tile_of(t);
+      const bool have = MODE != TN || tl.red > 0;
+      const int acc = i & 1;
+      const uint32_t aph = (i >> 1) & 1u;
+      if (have) {
+        ++i;
+        if (!warp_wait<false>(&sm.tmem_full[acc], aph, &sm.abort, p.status)) break;
+        ptx::tc_fence_after();
+      }
+      const uint32_t tbase = tmem_base + lane_addr + acc * BT;
+      if (MODE != TN) {
+        const int n = tl.m0 + q * 32 + lane;
+        const bool live = n < p.N;
+#pragma unroll 1
+        for (int c = 0; c < tl.count; c += 32) {
+          uint32_t v[32];
+          ptx::tmem_ld32(tbase + c, v);
+          const float rw = p.row_weight && c + lane < tl.count ? p.row_weight[tl.row0 + c + lane] : 1.0f;
+          ptx::tmem_ld_wait();
+          const int left = tl.count - c;
+          if (p.out_f32) {
+            float *y = (float *)p.out + (long)(tl.row0 + c) * p.N + n;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float w = __shfl_sync(0xffffffffu, rw, j);
+              if (live && j < left) y[(long)j * p.N] = __uint_as_float(v[j]) * w;
+            }
+          } else {
+            // two tokens at a time: the even lane takes features (n, n+1) of
+            // the first, the odd lane (n-1, n) of the second
+            const int odd = lane & 1;
+            __nv_bfloat16 *y = (__nv_bfloat16 *)p.out + (long)(tl.row0 + c + odd) * p.N + (n - odd);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float v0 = __uint_as_float(v[j]) * __shfl_sync(0xffffffffu, rw, j);
+              const float v1 = __uint_as_float(v[j + 1]) * __shfl_sync(0xffffffffu, rw, j + 1);
+              const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+              const __nv_bfloat162 o = odd ? __floats2bfloat162_rn(other, v1) : __floats2bfloat162_rn(v0, other);
+              if (live && j + odd < left) *reinterpret_cast<__nv_bfloat162 *>(y + (long)j * p.N) = o;
+            }
+          }
+        }
+      } else {
+        // rows of dW: 32 words of each lane's row at a time through this
+        // warp's 4 KB (16-byte piece j of row r at j ^ (r % 8)), so that every
+        // store writes four whole 128-byte row segments
+        uint32_t *stg = staging + q * 32 * 32;
+        const int n_first = tl.m0 + q * 32;
+        const int rr = lane >> 3, ff = lane & 7;
+        // words staged as fp32 sums, or as bf16 pairs already rounded (bf16
+        // out without a previous value to add: the sum is rounded once either way)
+        const bool fp32 = p.out_f32 || p.accumulate;
+        const int per = fp32 ? 32 : 64;  // columns per round
+#pragma unroll 1
+        for (int c = 0; c < tl.count; c += per) {
+          if (have) {
+            uint32_t v[32];
+            if (fp32) {
+              ptx::tmem_ld32(tbase + c, v);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4 *>(stg + lane * 32 + ((j ^ (lane & 7)) << 2)) =
+                    make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            } else {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                ptx::tmem_ld32(tbase + c + half * 32, v);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 o = __floats2bfloat162_rn(__uint_as_float(v[8 * j + 2 * k]),
+                                                                   __uint_as_float(v[8 * j + 2 * k + 1]));
+                    w[k] = *reinterpret_cast<const uint32_t *>(&o);
+                  }
+                  *reinterpret_cast<uint4 *>(stg + lane * 32 + (((half * 4 + j) ^ (lane & 7)) << 2)) =
+                      make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+            }
+            __syncwarp();
+          }
+          const int col = tl.c0 + c + ff * (fp32 ? 4 : 8);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + rr;
+            if (n_first + r >= p.N || col >= p.K || (!have && p.accumulate)) continue;
+            uint4 val = make_uint4(0, 0, 0, 0);
+            if (have) val = *reinterpret_cast<const uint4 *>(stg + r * 32 + ((ff ^ (r & 7)) << 2));
+            const long at = ((long)tl.e * p.N + n_first + r) * p.K + col;
+            if (!p.accumulate) {
+              *reinterpret_cast<uint4 *>((uint8_t *)p.out + at * (p.out_f32 ? 4 : 2)) = val;
+              continue;
+            }
+            const float4 sum = make_float4(__uint_as_float(val.x), __uint_as_float(val.y), __uint_as_float(val.z),
+                                           __uint_as_float(val.w));
+            if (p.out_f32) {
+              float4 *dst = reinterpret_cast<float4 *>((float *)p.out + at);
+              const float4 old = *dst;
+              *dst = make_float4(old.x + sum.x, old.y + sum.y, old.z + sum.z, old.w + sum.w);
+            } else {
+              uint2 *dst = reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.out + at);
+              const uint2 old = *dst;
+              const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&old.x));
+              const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&old.y));
+              const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x + sum.x, a.y + sum.y);
+              const __nv_bfloat162 hi = __floats2bfloat162_rn(b.x + sum.z, b.y + sum.w);
+              *dst = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (have) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.tmem_empty[acc]);
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+template <Mode MODE, int BT>
+moe_status launch(Params &p, const void *a, const void *b, cudaStream_t s) {
+  using C = Cfg<BT>;
+  CUtensorMap ta, tb;
+  bool ok;
+  if (MODE == NT) {
+    ok = tma_map_bf16(&ta, a, 3, (uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.E, BM) &&
+         tma_map_bf16(&tb, b, 2, (uint64_t)p.K, (uint64_t)p.rows, 1, TOK_BOX);
+  } else if (MODE == NN) {
+    ok = tma_map_bf16(&ta, a, 3, (uint64_t)p.N, (uint64_t)p.K, (uint64_t)p.E, BK) &&
+         tma_map_bf16(&tb, b, 2, (uint64_t)p.K, (uint64_t)p.rows, 1, TOK_BOX);
+  } else {
+    ok = tma_map_bf16(&ta, a, 2, (uint64_t)p.N, (uint64_t)p.rows, 1, BK) &&
+         tma_map_bf16(&tb, b, 2, (uint64_t)p.K, (uint64_t)p.rows, 1, BK);
+  }
+  if (!ok) return MOE_ERR_CUDA;
+  int dev = 0, sms = 148;
+  MOE_CUDA_TRY(cudaGetDevice(&dev));
+  MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  p.m_blocks = (p.N + BM - 1) / BM;
+  p.n_blocks = (p.K + BT - 1) / BT;
+  const long used = p.rows < p.E ? p.rows : p.E;  // groups with rows
+  const long tiles = MODE == TN ? (long)p.E * p.m_blocks * p.n_blocks
+                                : ((long)(p.rows + BT - 1) / BT + used) * p.m_blocks;  // at most
+  if (tiles > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
+  const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart + (MODE == TN ? kStaging : 0);
+  auto kern = grouped_gemm<MODE, BT>;
+  MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  kern<<<(int)(tiles < sms ? tiles : sms), kThreads, smem, s>>>(ta, tb, p);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status launch_grouped_bf16(const MoEGrouped &g, const void *a, const int32_t *offsets, const void *w,
+                               bool transposed, const float *row_weight, void *y, int *status, cudaStream_t s) {
+  Params p = {};
+  p.rows = g.rows;
+  p.N = g.n;
+  p.K = g.k;
+  p.E = g.groups;
+  p.offsets = offsets;
+  p.row_weight = row_weight;
+  p.out = y;
+  p.out_f32 = g.out_dtype == MOE_F32;
+  p.status = status;
+  // few rows a group: narrow token tiles leave the ring eight 16 KB weight
+  // stages instead of four
+  const bool narrow = g.rows <= 64l * g.groups;
+  if (transposed) return narrow ? launch<NN, 64>(p, w, a, s) : launch<NN, 256>(p, w, a, s);
+  return narrow ? launch<NT, 64>(p, w, a, s) : launch<NT, 256>(p, w, a, s);
+}
+
+moe_status launch_grouped_wgrad_bf16(const MoEGrouped &g, const void *dy, const void *a, const int32_t *offsets,
+                                     bool accumulate, void *dw, int *status, cudaStream_t s) {
+  Params p = {};
+  p.rows = g.rows;
+  p.N = g.n;
+  p.K = g.k;
+  p.E = g.groups;
+  p.offsets = offsets;
+  p.out = dw;
+  p.out_f32 = g.out_dtype == MOE_F32;
+  p.accumulate = accumulate;
+  p.status = status;
+  return launch<TN, 256>(p, dy, a, s);
+}
+
+}  // namespace moe

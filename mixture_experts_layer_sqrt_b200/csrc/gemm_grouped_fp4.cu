@@ -1,0 +1,447 @@
+// Product of two NVFP4 operands grouped by expert (tcgen05 block-scaled MMA):
+//
+//   y[r, n] = w_r * ra_r * rw_en * sum_k (qa[r, k] sa[r, k/16]) (qw[e, n, k] sw[e, n, k/16])
+//
+// for the rows r of group e: e2m1 codes q, an e4m3 scale per 16 of them, and
+// optional fp32 row scales of either operand.  The MMA multiplies codes and
+// scales exactly and accumulates in fp32; the row scales and the routing
+// weight enter in the epilogue.
+//
+// Layout of the work as in gemm_grouped.cu: weights on the MMA's M side (128
+// output features a tile), the tokens of one group on its N side (up to BT,
+// rounded to 16), so ragged groups pad nothing and the packed weights are read
+// once per BT tokens.  A stage holds 256 reduction elements: rows of 128 bytes
+// of codes (128-byte swizzle) and 16 bytes of scales.
+//
+// The MMA takes the scales from TMEM: for each 64 reduction elements one
+// 32-bit column per 32 rows (lane i of column j: the four scale bytes of row
+// 32 j + i), the same in all four lane quadrants.  Four warps, one a quadrant,
+// copy them there from the stage with tcgen05.st, one 16-byte read a row, a
+// stage ahead of the MMAs (two TMEM buffers).  Scale rows that TMA cannot read
+// (K not a multiple of 256: rows not a multiple of 16 bytes) are loaded by the
+// same warps from global memory, one stage ahead in registers.
+//
+// Roles (320 threads, persistent, one CTA per SM): warp 0 TMA producer, warp 1
+// TMEM owner and MMA issuer, warps 2-5 epilogue, warps 6-9 scales.  Every wait
+// is bounded.
+#include <cudaTypedefs.h>
+#include <limits.h>
+
+#include "grouped.cuh"
+#include "kernels.h"
+#include "tma_host.h"
+
+namespace moe {
+
+MOE_VIOLATION_COUNTER(violations_gemm_grouped_fp4)
+
+namespace {
+
+using namespace grouped;
+
+constexpr int BM = 128;                 // output features per tile
+constexpr int BK = 256;                 // reduction elements per stage
+constexpr int ROW = BK / 2;             // bytes of codes a row and stage
+constexpr int MMA_K = 64;
+constexpr int STEPS = BK / MMA_K;
+constexpr int TOK_BOX = 32;             // token rows per TMA box
+constexpr int kThreads = 320;
+constexpr int kScaleWarp0 = 6;
+
+template <int BT>
+struct Cfg {
+  static constexpr int A_BYTES = BM * ROW;
+  static constexpr int B_BYTES = BT * ROW;
+  static constexpr int SA_BYTES = BM * 16;
+  static constexpr int SB_BYTES = BT * 16;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
+  static constexpr int STAGES = BT == 192 ? 4 : 7;
+  static constexpr int SFA_COLS = STEPS * BM / 32;   // TMEM columns of a stage's scales
+  static constexpr int SFB_COLS = STEPS * BT / 32;
+  static constexpr int SF_COLS = SFA_COLS + SFB_COLS;
+  static constexpr int SF_BASE = 2 * BT;             // past the two accumulators
+  static constexpr uint32_t TMEM_COLS = BT == 192 ? 512 : 256;
+  static_assert(SF_BASE + 2 * SF_COLS <= (int)TMEM_COLS, "accumulators and scales fit in TMEM");
+};
+
+template <int STAGES>
+struct Smem {
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t sf_full[2];
+  uint64_t sf_empty[2];
+  uint64_t tmem_full[2];
+  uint64_t tmem_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int start[MAX_E + 1];
+};
+constexpr int kSmemPart = 4608;
+static_assert(sizeof(Smem<8>) <= kSmemPart, "barriers and tile list");
+
+struct Params {
+  int rows, N, K, E, m_blocks;
+  const int32_t *offsets;
+  const uint8_t *sa, *sw;     // scale rows, for the path without TMA
+  const float *ra, *rw;       // row scales [rows], [E, N], or null
+  const float *row_weight;    // [rows] or null
+  void *out;
+  int out_f32;
+  int *status;
+};
+
+// D (+)= (A sfA) (B sfB)^T: e2m1 operands, an e4m3 scale per 16; one thread issues.
+__device__ __forceinline__ void mma_nvfp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// This thread's TMEM lane, consecutive columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Instruction descriptor of kind::mxf4nvf4 without N: A and B e2m1 (code 1 at
+// [7,10) and [10,12)), both K-major, e4m3 scales (bit 23 = 0), M >> 7 at
+// [27,29), scale data ids 0, K = 64 (bit 31 = 0).
+constexpr uint32_t kIdesc0 = (1u << 7) | (1u << 10) | ((uint32_t)(BM >> 7) << 27);
+
+// Up to 16 scale bytes of a row, `left` of them present (a multiple of 2).
+__device__ __forceinline__ void load_scales(const uint8_t *p, int left, bool words, uint32_t (&w)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    w[k] = 0;
+    if (words) {  // rows a multiple of 4 bytes
+      if (4 * k < left) w[k] = __ldg(reinterpret_cast<const uint32_t *>(p) + k);
+    } else {
+      if (4 * k < left) w[k] = __ldg(reinterpret_cast<const uint16_t *>(p) + 2 * k);
+      if (4 * k + 2 < left) w[k] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(p) + 2 * k + 1) << 16;
+    }
+  }
+}
+
+template <int BT, bool SF_TMA>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_gemm_fp4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                     const Params p) {
+  using C = Cfg<BT>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *stage_a = base;
+  uint8_t *stage_b = stage_a + STAGES * C::A_BYTES;
+  uint8_t *stage_sa = stage_b + STAGES * C::B_BYTES;
+  uint8_t *stage_sb = stage_sa + STAGES * C::SA_BYTES;
+  Smem<STAGES> &sm = *reinterpret_cast<Smem<STAGES> *>(stage_sb + STAGES * C::SB_BYTES);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      ptx::mbar_init(&sm.full[s], 1);
+      ptx::mbar_init(&sm.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&sm.sf_full[a], 4);
+      ptx::mbar_init(&sm.sf_empty[a], 1);
+      ptx::mbar_init(&sm.tmem_full[a], 1);
+      ptx::mbar_init(&sm.tmem_empty[a], 4);
+    }
+    ptx::mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmB);
+    if (SF_TMA) {
+      ptx::prefetch_tmap(&tmSA);
+      ptx::prefetch_tmap(&tmSB);
+    }
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&sm.tmem_base, C::TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  if (warp == 2) {
+    const bool ok = scan_tiles(p.offsets, p.rows, p.E, BT, sm.start);
+    if (kChecked && !ok && lane == 0 && blockIdx.x == 0) note_violation();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = sm.tmem_base;
+  const int total = sm.start[p.E] * p.m_blocks;
+  const int kbs = (p.K + BK - 1) / BK;
+  auto tile_of = [&](int t) { return token_tile(sm.start, p.offsets, p.rows, p.E, p.m_blocks, t); };
+
+  if (warp == 0) {
+    // ================================================= TMA producer
+    if (lane == 0) {
+      Ring<STAGES> ring;
+      uint32_t issued = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const TokenTile tl = tile_of(t);
+        const int boxes = (tl.count + TOK_BOX - 1) / TOK_BOX;
+        const uint32_t tx = C::A_BYTES + boxes * TOK_BOX * ROW + (SF_TMA ? C::SA_BYTES + boxes * TOK_BOX * 16 : 0);
+        for (int kb = 0; kb < kbs; ++kb, ring.next(), ++issued) {
+          if (!wait_bar<true>(&sm.empty[ring.s], ring.ph ^ 1u, &sm.abort, p.status)) {
+            ok = false;
+            break;
+          }
+          uint64_t *bar = &sm.full[ring.s];
+          ptx::mbar_arrive_expect_tx(bar, tx);
+          ptx::tma_load_3d(stage_a + ring.s * C::A_BYTES, &tmA, bar, kb * ROW, tl.blk * BM, tl.e);
+          if (SF_TMA) ptx::tma_load_3d(stage_sa + ring.s * C::SA_BYTES, &tmSA, bar, kb * 16, tl.blk * BM, tl.e);
+          for (int i = 0; i < boxes; ++i) {
+            ptx::tma_load_3d(stage_b + ring.s * C::B_BYTES + i * TOK_BOX * ROW, &tmB, bar, kb * ROW,
+                             tl.row0 + i * TOK_BOX, 0);
+            if (SF_TMA)
+              ptx::tma_load_3d(stage_sb + ring.s * C::SB_BYTES + i * TOK_BOX * 16, &tmSB, bar, kb * 16,
+                               tl.row0 + i * TOK_BOX, 0);
+          }
+        }
+      }
+      for (int s = 0; s < STAGES; ++s) {
+        if ((uint32_t)s >= issued) break;
+        const uint32_t last = (issued - 1 - s) / STAGES;
+        drain_bar(&sm.full[s], last & 1u, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ================================================= MMA issuer
+    if (lane == 0) {
+      Ring<STAGES> ring;
+      Ring<2> sf;
+      int i = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++i) {
+        const TokenTile tl = tile_of(t);
+        const int acc = i & 1;
+        const uint32_t aph = (i >> 1) & 1u;
+        if (!wait_bar<false>(&sm.tmem_empty[acc], aph ^ 1u, &sm.abort, p.status)) break;
+        ptx::tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * BT;
+        const uint32_t idesc = kIdesc0 | (uint32_t)((tl.count + 15) >> 4) << 18;  // N >> 3 at bit 17
+        for (int kb = 0; kb < kbs; ++kb, ring.next(), sf.next()) {
+          if (!wait_bar<true>(&sm.full[ring.s], ring.ph, &sm.abort, p.status) ||
+              !wait_bar<true>(&sm.sf_full[sf.s], sf.ph, &sm.abort, p.status)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t aa = ptx::smem_addr(stage_a + ring.s * C::A_BYTES);
+          const uint32_t ba = ptx::smem_addr(stage_b + ring.s * C::B_BYTES);
+          const uint32_t sfa = tmem_base + C::SF_BASE + sf.s * C::SF_COLS, sfb = sfa + C::SFA_COLS;
+#pragma unroll
+          for (int k = 0; k < STEPS; ++k)
+            mma_nvfp4(d_tmem, ptx::desc_kmajor_sw128(aa + k * MMA_K / 2), ptx::desc_kmajor_sw128(ba + k * MMA_K / 2),
+                      idesc, sfa + k * (BM / 32), sfb + k * (BT / 32), (kb | k) != 0);
+          ptx::mma_commit(&sm.empty[ring.s]);
+          ptx::mma_commit(&sm.sf_empty[sf.s]);
+        }
+        if (ok) ptx::mma_commit(&sm.tmem_full[acc]);
+      }
+      ptx::mma_commit(&sm.drain);
+      drain_bar(&sm.drain, 0, p.status);
+    }
+    __syncwarp();
+  } else if (warp >= kScaleWarp0) {
+    // ================================================= scales to TMEM
+    const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+    constexpr int AR = BM / 32, BR = BT / 32;  // rows of each operand a lane
+    const bool words = (p.K & 63) == 0;
+    const int pitch = p.K / 16;
+    Ring<STAGES> ring;
+    Ring<2> sf;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const TokenTile tl = tile_of(t);
+      uint32_t va[AR][4], vb[BR][4];
+      auto fetch = [&](int kb) {  // the path without TMA
+        const int left = pitch - kb * 16;
+#pragma unroll
+        for (int j = 0; j < AR; ++j) {
+          const int n = tl.blk * BM + j * 32 + lane;
+          load_scales(p.sw + ((long)tl.e * p.N + n) * pitch + kb * 16, n < p.N ? left : 0, words, va[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < BR; ++j) {
+          const int r = j * 32 + lane;
+          load_scales(p.sa + (long)(tl.row0 + r) * pitch + kb * 16, r < tl.count ? left : 0, words, vb[j]);
+        }
+      };
+      if (!SF_TMA) fetch(0);
+      for (int kb = 0; kb < kbs; ++kb, ring.next(), sf.next()) {
+        if (SF_TMA) {
+          if (!warp_wait<true>(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) {
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          const uint4 *a = reinterpret_cast<const uint4 *>(stage_sa + ring.s * C::SA_BYTES) + lane;
+          const uint4 *b = reinterpret_cast<const uint4 *>(stage_sb + ring.s * C::SB_BYTES) + lane;
+#pragma unroll
+          for (int j = 0; j < AR; ++j) {
+            const uint4 v = a[j * 32];
+            va[j][0] = v.x, va[j][1] = v.y, va[j][2] = v.z, va[j][3] = v.w;
+          }
+#pragma unroll
+          for (int j = 0; j < BR; ++j) {
+            const uint4 v = b[j * 32];
+            vb[j][0] = v.x, vb[j][1] = v.y, vb[j][2] = v.z, vb[j][3] = v.w;
+          }
+        }
+        if (!warp_wait<true>(&sm.sf_empty[sf.s], sf.ph ^ 1u, &sm.abort, p.status)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        uint32_t ca[C::SFA_COLS], cb[C::SFB_COLS];
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+#pragma unroll
+          for (int j = 0; j < AR; ++j) ca[k * AR + j] = va[j][k];
+#pragma unroll
+          for (int j = 0; j < BR; ++j) cb[k * BR + j] = vb[j][k];
+        }
+        const uint32_t at = tmem_base + lane_addr + C::SF_BASE + sf.s * C::SF_COLS;
+#pragma unroll
+        for (int c = 0; c < C::SFA_COLS; c += 8) tmem_st8(at + c, ca + c);
+#pragma unroll
+        for (int c = 0; c < C::SFB_COLS; c += 8) tmem_st8(at + C::SFA_COLS + c, cb + c);
+        if (!SF_TMA && kb + 1 < kbs) fetch(kb + 1);
+        tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.sf_full[sf.s]);
+      }
+    }
+  } else {
+    // ================================================= epilogue (warps 2..5)
+    const int q = warp & 3;
+    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    int i = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x, ++i) {
+      const TokenTile tl = tile_of(t);
+      const int acc = i & 1;
+      const uint32_t aph = (i >> 1) & 1u;
+      const int n = tl.blk * BM + q * 32 + lane;
+      const bool live = n < p.N;
+      const float wn = p.rw && live ? p.rw[(long)tl.e * p.N + n] : 1.0f;
+      if (!warp_wait<false>(&sm.tmem_full[acc], aph, &sm.abort, p.status)) break;
+      ptx::tc_fence_after();
+      const uint32_t tbase = tmem_base + lane_addr + acc * BT;
+#pragma unroll 1
+      for (int c = 0; c < tl.count; c += 32) {
+        uint32_t v[32];
+        ptx::tmem_ld32(tbase + c, v);
+        float rs = 1.0f;
+        if (c + lane < tl.count) {
+          const int r = tl.row0 + c + lane;
+          if (p.ra) rs = p.ra[r];
+          if (p.row_weight) rs *= p.row_weight[r];
+        }
+        ptx::tmem_ld_wait();
+        const int left = tl.count - c;
+        if (p.out_f32) {
+          float *y = (float *)p.out + (long)(tl.row0 + c) * p.N + n;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float w = __shfl_sync(0xffffffffu, rs, j);
+            if (live && j < left) y[(long)j * p.N] = __uint_as_float(v[j]) * wn * w;
+          }
+        } else {
+          const int odd = lane & 1;
+          __nv_bfloat16 *y = (__nv_bfloat16 *)p.out + (long)(tl.row0 + c + odd) * p.N + (n - odd);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float v0 = __uint_as_float(v[j]) * wn * __shfl_sync(0xffffffffu, rs, j);
+            const float v1 = __uint_as_float(v[j + 1]) * wn * __shfl_sync(0xffffffffu, rs, j + 1);
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+            const __nv_bfloat162 o = odd ? __floats2bfloat162_rn(other, v1) : __floats2bfloat162_rn(v0, other);
+            if (live && j + odd < left) *reinterpret_cast<__nv_bfloat162 *>(y + (long)j * p.N) = o;
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.tmem_empty[acc]);
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+template <int BT, bool SF_TMA>
+moe_status launch(Params &p, const void *a, const void *w, cudaStream_t s) {
+  using C = Cfg<BT>;
+  CUtensorMap ta, tb, tsa, tsb;
+  if (!tma_map_u8(&ta, w, (uint64_t)p.K / 2, p.N, p.E, ROW, BM, 128) ||
+      !tma_map_u8(&tb, a, (uint64_t)p.K / 2, p.rows, 1, ROW, TOK_BOX, 128))
+    return MOE_ERR_CUDA;
+  tsa = ta;
+  tsb = tb;
+  if (SF_TMA && (!tma_map_u8(&tsa, p.sw, (uint64_t)p.K / 16, p.N, p.E, 16, BM) ||
+                 !tma_map_u8(&tsb, p.sa, (uint64_t)p.K / 16, p.rows, 1, 16, TOK_BOX)))
+    return MOE_ERR_CUDA;
+  int dev = 0, sms = 148;
+  MOE_CUDA_TRY(cudaGetDevice(&dev));
+  MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  p.m_blocks = (p.N + BM - 1) / BM;
+  const long used = p.rows < p.E ? p.rows : p.E;
+  const long tiles = ((long)(p.rows + BT - 1) / BT + used) * p.m_blocks;
+  if (tiles > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
+  const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart;
+  auto kern = grouped_gemm_fp4<BT, SF_TMA>;
+  MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  kern<<<(int)(tiles < sms ? tiles : sms), kThreads, smem, s>>>(ta, tb, tsa, tsb, p);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status launch_grouped_nvfp4(const MoEGrouped &g, const void *a, const void *sa, const float *ra,
+                                const int32_t *offsets, const void *w, const void *sw, const float *rw,
+                                const float *row_weight, void *y, int *status, cudaStream_t s) {
+  Params p = {};
+  p.rows = g.rows;
+  p.N = g.n;
+  p.K = g.k;
+  p.E = g.groups;
+  p.offsets = offsets;
+  p.sa = (const uint8_t *)sa;
+  p.sw = (const uint8_t *)sw;
+  p.ra = ra;
+  p.rw = rw;
+  p.row_weight = row_weight;
+  p.out = y;
+  p.out_f32 = g.out_dtype == MOE_F32;
+  p.status = status;
+  const bool narrow = g.rows <= 64l * g.groups;  // as in gemm_grouped.cu
+  const bool sf_tma = g.k % 256 == 0;
+  if (narrow) return sf_tma ? launch<64, true>(p, a, w, s) : launch<64, false>(p, a, w, s);
+  return sf_tma ? launch<192, true>(p, a, w, s) : launch<192, false>(p, a, w, s);
+}
+
+}  // namespace moe

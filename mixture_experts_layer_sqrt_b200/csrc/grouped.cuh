@@ -1,0 +1,144 @@
+// What the grouped products (gemm_grouped.cu, gemm_grouped_fp4.cu,
+// gemm_grouped_f32.cu) share: bounded waits of the tensor-core pipelines and
+// the rows of a group.  Internal to libmoe_b200.
+#pragma once
+
+#include "common.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace grouped {
+
+constexpr int MAX_E = 1024;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+constexpr uint64_t kDrainLimitNs = 200000000ull;  // 0.2 s
+
+// Bounded wait; false if the CTA is aborting (this thread may have started
+// it).  SPIN for the hand-offs on the k-block path; the others sleep on the
+// barrier with a suspend-time hint.
+template <bool SPIN>
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int *abort_flag, int *status) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t n = 1;; ++n) {
+    if (SPIN ? ptx::mbar_try_wait(bar, parity) : ptx::mbar_try_wait_sleep(bar, parity, ptx::kWaitHintNs)) return true;
+    if (SPIN && (n & 63u) != 0) continue;
+    if (*(volatile int *)abort_flag) return false;
+    if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+      *(volatile int *)abort_flag = 1;
+      atomicExch(status, kDevTimeout);
+      return false;
+    }
+  }
+}
+
+// Warp-uniform wait: lane 0 polls, the outcome is broadcast to the warp.
+template <bool SPIN>
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *abort_flag, int *status) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait_bar<SPIN>(bar, parity, abort_flag, status);
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+// Used while winding down: copies and MMAs already issued must land first.
+__device__ __forceinline__ void drain_bar(uint64_t *bar, uint32_t parity, int *status) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (ptx::globaltimer_ns() - t0 > kDrainLimitNs) {
+      atomicExch(status, kDevTimeout);
+      return;
+    }
+  }
+}
+
+// Place in a ring of N stages: the stage and the parity of its current round.
+template <int N>
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// Rows [begin, end) of group e, kept within [0, rows] whatever the offsets
+// hold, so that offsets out of range cannot lead to an access out of range.
+// offsets == null: one group of all rows.
+__device__ __forceinline__ int clamp_row(int v, int rows) { return v < 0 ? 0 : (v > rows ? rows : v); }
+__device__ __forceinline__ int seg_begin(const int32_t *offsets, int rows, int e) {
+  return offsets ? clamp_row(offsets[e], rows) : 0;
+}
+__device__ __forceinline__ int seg_end(const int32_t *offsets, int rows, int e) {
+  return offsets ? clamp_row(offsets[e + 1], rows) : rows;
+}
+
+// One warp: start[e] = sum over e' < e of ceil(rows_e' / tile_rows), e = 0..E
+// (the last entry is the total).  Checked build: false if an offset is below
+// 0 or the offsets decrease, and then every group counts as empty.
+__device__ __forceinline__ bool scan_tiles(const int32_t *offsets, int rows, int E, int tile_rows, int *start) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  bool bad = false;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    int v = 0;
+    if (e < E) {
+      const int n = seg_end(offsets, rows, e) - seg_begin(offsets, rows, e);
+      if (kChecked && offsets && (offsets[e] < 0 || offsets[e + 1] < offsets[e])) bad = true;
+      v = n > 0 ? (n + tile_rows - 1) / tile_rows : 0;
+    }
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    if (e < E) start[e] = carry + incl - v;
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  const bool any_bad = kChecked && __any_sync(0xffffffffu, bad);
+  if (any_bad) {
+    for (int e = lane; e < E; e += 32) start[e] = 0;
+    carry = 0;
+  }
+  if (lane == 0) start[E] = carry;
+  return !any_bad;
+}
+
+// Largest e with start[e] * per <= t (empty groups share the next start).
+__device__ __forceinline__ int find_group(const int *start, int E, int per, int t) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] * per <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A tile of tokens: group e's rows are cut into as few tiles of at most
+// tile_rows as hold them, of nearly equal widths (multiples of 16, the MMA's
+// N step), so that 300 rows are 160 + 140 and not 256 + 44.
+struct TokenTile {
+  int e, blk, row0, count;  // group, output-feature block, first row, rows
+};
+__device__ __forceinline__ TokenTile token_tile(const int *start, const int32_t *offsets, int rows, int E, int blocks,
+                                                int t) {
+  TokenTile r;
+  r.e = find_group(start, E, blocks, t);
+  const int tiles = start[r.e + 1] - start[r.e];
+  const int local = t - start[r.e] * blocks;
+  r.blk = local / tiles;
+  const int j = local - r.blk * tiles;
+  const int begin = seg_begin(offsets, rows, r.e), end = seg_end(offsets, rows, r.e);
+  const int width = ((end - begin + tiles - 1) / tiles + 15) & ~15;
+  r.row0 = begin + j * width;
+  r.count = end - r.row0 < width ? end - r.row0 : width;
+  return r;
+}
+
+}  // namespace grouped
+}  // namespace moe

@@ -90,6 +90,33 @@ moe_status launch_down_fp4(const MoEConfig &c, int rows, const void *h, const in
 // either below 65504.
 inline bool h_fits_f16(const MoEConfig &c) { return c.swiglu_clamp > 0.0f && c.swiglu_clamp <= 255.0f; }
 
+// gemm_grouped.cu, gemm_grouped_f32.cu, gemm_grouped_fp4.cu ----------------
+// moe_grouped_matmul, moe_grouped_wgrad and moe_grouped_matmul_nvfp4 for
+// checked arguments with rows > 0.
+moe_status launch_grouped_bf16(const MoEGrouped &g, const void *a, const int32_t *offsets, const void *w,
+                               bool transposed, const float *row_weight, void *y, int *status, cudaStream_t s);
+moe_status launch_grouped_wgrad_bf16(const MoEGrouped &g, const void *dy, const void *a, const int32_t *offsets,
+                                     bool accumulate, void *dw, int *status, cudaStream_t s);
+moe_status launch_grouped_f32(const MoEGrouped &g, const void *a, const int32_t *offsets, const void *w,
+                              bool transposed, const float *row_weight, void *y, cudaStream_t s);
+moe_status launch_grouped_wgrad_f32(const MoEGrouped &g, const void *dy, const void *a, const int32_t *offsets,
+                                    bool accumulate, void *dw, cudaStream_t s);
+moe_status launch_grouped_nvfp4(const MoEGrouped &g, const void *a, const void *sa, const float *ra,
+                                const int32_t *offsets, const void *w, const void *sw, const float *rw,
+                                const float *row_weight, void *y, int *status, cudaStream_t s);
+
+// quantize.cu --------------------------------------------------------------
+moe_status launch_quantize_nvfp4(int rows, int cols, moe_dtype dtype, bool swiglu, const void *src, int src_rows,
+                                 const int32_t *row_token, const int32_t *live, float limit, int mode, void *codes,
+                                 void *scales, float *row_scale, void *values, cudaStream_t s);
+
+// swiglu.cu ----------------------------------------------------------------
+moe_status launch_swiglu(int rows, int F, moe_dtype dtype, const void *gu, float limit, int mode, const int32_t *live,
+                         void *h, cudaStream_t s);
+moe_status launch_swiglu_backward(int rows, int F, moe_dtype dtype, const void *gu, const void *dh,
+                                  const float *row_weight, float limit, int mode, const int32_t *live, void *dgu,
+                                  void *hw, float *drow_weight, cudaStream_t s);
+
 // One block whose bounded wait never completes: records the timeout status.
 moe_status launch_wait_selftest(int *status, cudaStream_t s);
 
@@ -100,6 +127,10 @@ unsigned int violations_combine();
 unsigned int violations_gemm_tc();
 unsigned int violations_gemm_fp4();
 unsigned int violations_gemm_simt();
+unsigned int violations_gemm_grouped();
+unsigned int violations_gemm_grouped_f32();
+unsigned int violations_gemm_grouped_fp4();
+unsigned int violations_quantize();
 
 // dequant.cu -------------------------------------------------------------
 // n_elems values (a multiple of 16): packed [n/2] bytes + scales [n/16] -> bf16 [n].
