@@ -24,12 +24,13 @@
 // are set to zero in both operands before the MMAs read them, so that nothing
 // there, NaN included, reaches this group's sum.
 //
-// Roles (192 threads per CTA, persistent, one CTA per SM):
+// Roles (192 threads per CTA, 224 for TN; persistent, one CTA per SM):
 //   warp 0    TMA producer into the stage ring
 //   warp 1    TMEM owner; one thread issues the MMAs (4 x K=16 per stage);
 //             two accumulators let the epilogue of tile i overlap the MMAs
-//             of tile i+1.  TN: the warp first clears the lines above.
-//   warps 2-5 epilogue: TMEM lane = output feature.
+//             of tile i+1
+//   warps 2-5 epilogue: TMEM lane = output feature
+//   warp 6    TN: clears the lines above and hands every stage on to the MMAs
 //
 // Every wait is bounded (2 s, then MOE_ERR_DEVICE_TIMEOUT in the status word
 // and an orderly wind down).
@@ -55,8 +56,6 @@ constexpr int BK = 64;               // reduction elements per stage
 constexpr int UMMA_K = 16;
 constexpr int A_BYTES = BM * BK * 2;  // 16 KB
 constexpr int BOX = 64 * BK * 2;     // 8 KB: an MN-major box
-constexpr int TOK_BOX = 32;          // token rows per TMA box (NT, NN)
-constexpr int kThreads = 192;
 
 // BT: tokens (NT, NN) or columns (TN) per tile, the MMA's largest N.
 template <int BT>
@@ -64,12 +63,17 @@ struct Cfg {
   static constexpr int B_BYTES = BT * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int STAGES = BT == 256 ? 4 : 8;
+  static constexpr int TOK_BOX = BT == 256 ? 64 : 32;  // token rows per TMA box (NT, NN)
   static constexpr uint32_t TMEM_COLS = 2 * BT;
 };
+template <Mode MODE>
+constexpr int kThreads = MODE == TN ? 224 : 192;
+constexpr int kClearWarp = 6;  // TN
 
 template <int STAGES>
 struct Smem {
-  uint64_t full[STAGES];
+  uint64_t full[STAGES];    // stage ready for the MMAs
+  uint64_t landed[STAGES];  // TN: its copies are complete
   uint64_t empty[STAGES];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
@@ -109,7 +113,7 @@ __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr) {
 }
 
 template <Mode MODE, int BT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<MODE>, 1)
     grouped_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
   using C = Cfg<BT>;
   constexpr int STAGES = C::STAGES;
@@ -125,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       ptx::mbar_init(&sm.full[s], 1);
+      ptx::mbar_init(&sm.landed[s], 1);
       ptx::mbar_init(&sm.empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -190,21 +195,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ================================================= TMA producer
-    if (lane == 0) {
+    if (elect_one()) {
+      uint64_t *const bars = MODE == TN ? sm.landed : sm.full;
       Ring<STAGES> ring;
       uint32_t issued = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
         const Tile tl = tile_of(t);
         const int kbs = (tl.red + BK - 1) / BK;
-        const int boxes = MODE == TN ? (tl.count + 63) / 64 : (tl.count + TOK_BOX - 1) / TOK_BOX;
-        const uint32_t tx = A_BYTES + (uint32_t)boxes * (MODE == TN ? BOX : TOK_BOX * BK * 2);
+        const int boxes = MODE == TN ? (tl.count + 63) / 64 : (tl.count + C::TOK_BOX - 1) / C::TOK_BOX;
+        const uint32_t tx = A_BYTES + (uint32_t)boxes * (MODE == TN ? BOX : C::TOK_BOX * BK * 2);
         for (int kb = 0; kb < kbs; ++kb, ring.next(), ++issued) {
-          if (!wait_bar<true>(&sm.empty[ring.s], ring.ph ^ 1u, &sm.abort, p.status)) {
+          if (!wait_bar(&sm.empty[ring.s], ring.ph ^ 1u, &sm.abort, p.status)) {
             ok = false;
             break;
           }
-          uint64_t *bar = &sm.full[ring.s];
+          uint64_t *bar = &bars[ring.s];
           uint8_t *a = stage_a + ring.s * A_BYTES;
           uint8_t *b = stage_b + ring.s * C::B_BYTES;
           const int k0 = kb * BK;
@@ -220,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           for (int i = 0; i < boxes; ++i) {
             if (MODE == TN) ptx::tma_load_2d(b + i * BOX, &tmB, bar, tl.c0 + i * 64, tl.row0 + k0);
-            else ptx::tma_load_2d(b + i * TOK_BOX * BK * 2, &tmB, bar, k0, tl.row0 + i * TOK_BOX);
+            else ptx::tma_load_2d(b + i * C::TOK_BOX * BK * 2, &tmB, bar, k0, tl.row0 + i * C::TOK_BOX);
           }
         }
       }
@@ -228,73 +234,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < STAGES; ++s) {
         if ((uint32_t)s >= issued) break;
         const uint32_t last = (issued - 1 - s) / STAGES;  // this stage's last round
-        drain_bar(&sm.full[s], last & 1u, p.status);
+        drain_bar(&bars[s], last & 1u, p.status);
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ================================================= MMA issuer
-    // D fp32, A and B bf16; bit 15: A is MN-major, bit 16: B is
-    constexpr uint32_t idesc0 =
-        ptx::idesc_bf16_f32(BM, 0) | (MODE != NT ? 1u << 15 : 0u) | (MODE == TN ? 1u << 16 : 0u);
-    Ring<STAGES> ring;
-    int i = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const Tile tl = tile_of(t);
-      const int kbs = (tl.red + BK - 1) / BK;
-      if (kbs == 0) continue;  // TN, empty group: the epilogue needs no sum
-      const int acc = i & 1;
-      const uint32_t aph = (i >> 1) & 1u;
-      ++i;
-      if (!warp_wait<false>(&sm.tmem_empty[acc], aph ^ 1u, &sm.abort, p.status)) break;
-      ptx::tc_fence_after();
-      const uint32_t d_tmem = tmem_base + acc * BT;
-      const uint32_t idesc = idesc0 | (uint32_t)((tl.count + 15) >> 4) << 18;  // N >> 3 at bit 17, N a multiple of 16
-      for (int kb = 0; kb < kbs; ++kb, ring.next()) {
-        if (!warp_wait<true>(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) {
-          ok = false;
-          break;
-        }
-        uint8_t *a = stage_a + ring.s * A_BYTES;
-        uint8_t *b = stage_b + ring.s * C::B_BYTES;
-        const int left = tl.red - kb * BK;
-        int steps = BK / UMMA_K;
-        if (MODE == TN && left < BK) {
-          // lines [left, steps * 16) of every box belong to other rows
-          steps = (left + UMMA_K - 1) / UMMA_K;
-          const int lines = steps * UMMA_K - left;
-          __syncwarp();  // the copies that lane 0 saw land are ordered before every lane's stores
-          const int boxes = (tl.count + 63) / 64;
-          for (int j = lane; j < lines * 8 * (2 + boxes); j += 32) {
-            const int box = j / (lines * 8), in = j - box * lines * 8;
-            uint8_t *q = (box < 2 ? a + box * BOX : b + (box - 2) * BOX) + left * 128 + in * 16;
-            *reinterpret_cast<uint4 *>(q) = make_uint4(0, 0, 0, 0);
+    if (elect_one()) {
+      // D fp32, A and B bf16; bit 15: A is MN-major, bit 16: B is
+      constexpr uint32_t idesc0 =
+          ptx::idesc_bf16_f32(BM, 0) | (MODE != NT ? 1u << 15 : 0u) | (MODE == TN ? 1u << 16 : 0u);
+      // descriptors of stage 0; an address moves by its bytes >> 4
+      const uint64_t ad0 = MODE == NT ? ptx::desc_kmajor_sw128(ptx::smem_addr(stage_a))
+                                      : desc_mnmajor_sw128(ptx::smem_addr(stage_a));
+      const uint64_t bd0 = MODE == TN ? desc_mnmajor_sw128(ptx::smem_addr(stage_b))
+                                      : ptx::desc_kmajor_sw128(ptx::smem_addr(stage_b));
+      constexpr uint32_t a_step = (MODE == NT ? UMMA_K * 2 : UMMA_K * 128) >> 4;
+      constexpr uint32_t b_step = (MODE == TN ? UMMA_K * 128 : UMMA_K * 2) >> 4;
+      Ring<STAGES> ring;
+      bool ready = false;  // the next stage's barrier, read ahead of the MMAs before it
+      int i = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const Tile tl = tile_of(t);
+        const int kbs = (tl.red + BK - 1) / BK;
+        if (kbs == 0) continue;  // TN, empty group: the epilogue needs no sum
+        const int acc = i & 1;
+        const uint32_t aph = (i >> 1) & 1u;
+        ++i;
+        if (!wait_bar(&sm.tmem_empty[acc], aph ^ 1u, &sm.abort, p.status)) break;
+        ptx::tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * BT;
+        const uint32_t idesc = idesc0 | (uint32_t)((tl.count + 15) >> 4) << 18;  // N >> 3 at bit 17, N a multiple of 16
+        for (int kb = 0; kb < kbs; ++kb) {
+          if (!ready && !wait_bar(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) {
+            ok = false;
+            break;
           }
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (lane == 0) {
           ptx::tc_fence_after();
-          const uint32_t aa = ptx::smem_addr(a), ba = ptx::smem_addr(b);
-          for (int k = 0; k < steps; ++k) {
-            const uint64_t ad = MODE == NT ? ptx::desc_kmajor_sw128(aa + k * UMMA_K * 2)
-                                           : desc_mnmajor_sw128(aa + k * UMMA_K * 128);
-            const uint64_t bd = MODE == TN ? desc_mnmajor_sw128(ba + k * UMMA_K * 128)
-                                           : ptx::desc_kmajor_sw128(ba + k * UMMA_K * 2);
-            ptx::mma_bf16(d_tmem, ad, bd, idesc, (kb | k) != 0);
+          Ring<STAGES> nx = ring;
+          nx.next();
+          ready = ptx::mbar_try_wait(&sm.full[nx.s], nx.ph);
+          const uint64_t ad = ad0 + (uint32_t)ring.s * (A_BYTES >> 4), bd = bd0 + (uint32_t)ring.s * (C::B_BYTES >> 4);
+          const int left = tl.red - kb * BK;
+          if (MODE == TN && left <= BK - UMMA_K) {
+            const int steps = (left + UMMA_K - 1) / UMMA_K;
+            for (int k = 0; k < steps; ++k)
+              ptx::mma_bf16(d_tmem, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < BK / UMMA_K; ++k)
+              ptx::mma_bf16(d_tmem, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
           }
           ptx::mma_commit(&sm.empty[ring.s]);
+          ring = nx;
         }
-        __syncwarp();
+        if (ok) ptx::mma_commit(&sm.tmem_full[acc]);
       }
-      if (ok && lane == 0) ptx::mma_commit(&sm.tmem_full[acc]);
-      __syncwarp();
-    }
-    if (lane == 0) {  // all issued MMAs complete before TMEM is released
+      // all issued MMAs complete before TMEM is released
       ptx::mma_commit(&sm.drain);
       drain_bar(&sm.drain, 0, p.status);
     }
     __syncwarp();
+  } else if (MODE == TN && warp == kClearWarp) {
+    // ================================================= lines of other rows (TN)
+    Ring<STAGES> ring;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const Tile tl = tile_of(t);
+      const int kbs = (tl.red + BK - 1) / BK;
+      const int boxes = (tl.count + 63) / 64;
+      for (int kb = 0; kb < kbs; ++kb, ring.next()) {
+        if (!warp_wait(&sm.landed[ring.s], ring.ph, &sm.abort, p.status)) {
+          ok = false;
+          break;
+        }
+        const int left = tl.red - kb * BK;
+        if (left < BK) {  // lines [left, the MMAs' last) of every box
+          uint8_t *a = stage_a + ring.s * A_BYTES, *b = stage_b + ring.s * C::B_BYTES;
+          const int pieces = (((left + UMMA_K - 1) & ~(UMMA_K - 1)) - left) * 8;  // of 16 bytes, a box
+          for (int j = lane; j < pieces * (2 + boxes); j += 32) {
+            const int box = j / pieces, in = j - box * pieces;
+            uint8_t *q = (box < 2 ? a + box * BOX : b + (box - 2) * BOX) + left * 128 + in * 16;
+            *reinterpret_cast<uint4 *>(q) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.full[ring.s]);
+      }
+    }
   } else {
     // ================================================= epilogue (warps 2..5)
     const int q = warp & 3;  // TMEM lane quadrant this warp may access
@@ -307,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t aph = (i >> 1) & 1u;
       if (have) {
         ++i;
-        if (!warp_wait<false>(&sm.tmem_full[acc], aph, &sm.abort, p.status)) break;
+        if (!warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status)) break;
         ptx::tc_fence_after();
       }
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
@@ -442,10 +471,10 @@ moe_status launch(Params &p, const void *a, const void *b, cudaStream_t s) {
   bool ok;
   if (MODE == NT) {
     ok = tma_map_bf16(&ta, a, 3, (uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.E, BM) &&
-         tma_map_bf16(&tb, b, 2, (uint64_t)p.K, (uint64_t)p.rows, 1, TOK_BOX);
+         tma_map_bf16(&tb, b, 2, (uint64_t)p.K, (uint64_t)p.rows, 1, C::TOK_BOX);
   } else if (MODE == NN) {
     ok = tma_map_bf16(&ta, a, 3, (uint64_t)p.N, (uint64_t)p.K, (uint64_t)p.E, BK) &&
-         tma_map_bf16(&tb, b, 2, (uint64_t)p.K, (uint64_t)p.rows, 1, TOK_BOX);
+         tma_map_bf16(&tb, b, 2, (uint64_t)p.K, (uint64_t)p.rows, 1, C::TOK_BOX);
   } else {
     ok = tma_map_bf16(&ta, a, 2, (uint64_t)p.N, (uint64_t)p.rows, 1, BK) &&
          tma_map_bf16(&tb, b, 2, (uint64_t)p.K, (uint64_t)p.rows, 1, BK);
@@ -463,7 +492,7 @@ moe_status launch(Params &p, const void *a, const void *b, cudaStream_t s) {
   const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart + (MODE == TN ? kStaging : 0);
   auto kern = grouped_gemm<MODE, BT>;
   MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  kern<<<(int)(tiles < sms ? tiles : sms), kThreads, smem, s>>>(ta, tb, p);
+  kern<<<(int)(tiles < sms ? tiles : sms), kThreads<MODE>, smem, s>>>(ta, tb, p);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ================================================= TMA producer
-    if (lane == 0) {
+    if (elect_one()) {
       Ring<STAGES> ring;
       uint32_t issued = 0;
       bool ok = true;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int boxes = (tl.count + TOK_BOX - 1) / TOK_BOX;
         const uint32_t tx = C::A_BYTES + boxes * TOK_BOX * ROW + (SF_TMA ? C::SA_BYTES + boxes * TOK_BOX * 16 : 0);
         for (int kb = 0; kb < kbs; ++kb, ring.next(), ++issued) {
-          if (!wait_bar<true>(&sm.empty[ring.s], ring.ph ^ 1u, &sm.abort, p.status)) {
+          if (!wait_bar(&sm.empty[ring.s], ring.ph ^ 1u, &sm.abort, p.status)) {
             ok = false;
             break;
           }
@@ -220,37 +220,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         drain_bar(&sm.full[s], last & 1u, p.status);
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ================================================= MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
+      const uint64_t ad0 = ptx::desc_kmajor_sw128(ptx::smem_addr(stage_a));
+      const uint64_t bd0 = ptx::desc_kmajor_sw128(ptx::smem_addr(stage_b));
       Ring<STAGES> ring;
       Ring<2> sf;
+      bool ready = false, sf_ready = false;  // the next stage's barriers, read ahead
       int i = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++i) {
         const TokenTile tl = tile_of(t);
         const int acc = i & 1;
         const uint32_t aph = (i >> 1) & 1u;
-        if (!wait_bar<false>(&sm.tmem_empty[acc], aph ^ 1u, &sm.abort, p.status)) break;
+        if (!wait_bar(&sm.tmem_empty[acc], aph ^ 1u, &sm.abort, p.status)) break;
         ptx::tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BT;
         const uint32_t idesc = kIdesc0 | (uint32_t)((tl.count + 15) >> 4) << 18;  // N >> 3 at bit 17
-        for (int kb = 0; kb < kbs; ++kb, ring.next(), sf.next()) {
-          if (!wait_bar<true>(&sm.full[ring.s], ring.ph, &sm.abort, p.status) ||
-              !wait_bar<true>(&sm.sf_full[sf.s], sf.ph, &sm.abort, p.status)) {
+        for (int kb = 0; kb < kbs; ++kb) {
+          if ((!ready && !wait_bar(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) ||
+              (!sf_ready && !wait_bar(&sm.sf_full[sf.s], sf.ph, &sm.abort, p.status))) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t aa = ptx::smem_addr(stage_a + ring.s * C::A_BYTES);
-          const uint32_t ba = ptx::smem_addr(stage_b + ring.s * C::B_BYTES);
+          Ring<STAGES> nx = ring;
+          nx.next();
+          Ring<2> sn = sf;
+          sn.next();
+          ready = ptx::mbar_try_wait(&sm.full[nx.s], nx.ph);
+          sf_ready = ptx::mbar_try_wait(&sm.sf_full[sn.s], sn.ph);
+          const uint64_t ad = ad0 + (uint32_t)ring.s * (C::A_BYTES >> 4), bd = bd0 + (uint32_t)ring.s * (C::B_BYTES >> 4);
           const uint32_t sfa = tmem_base + C::SF_BASE + sf.s * C::SF_COLS, sfb = sfa + C::SFA_COLS;
 #pragma unroll
           for (int k = 0; k < STEPS; ++k)
-            mma_nvfp4(d_tmem, ptx::desc_kmajor_sw128(aa + k * MMA_K / 2), ptx::desc_kmajor_sw128(ba + k * MMA_K / 2),
-                      idesc, sfa + k * (BM / 32), sfb + k * (BT / 32), (kb | k) != 0);
+            mma_nvfp4(d_tmem, ad + k * (MMA_K / 2 >> 4), bd + k * (MMA_K / 2 >> 4), idesc, sfa + k * (BM / 32),
+                      sfb + k * (BT / 32), (kb | k) != 0);
           ptx::mma_commit(&sm.empty[ring.s]);
           ptx::mma_commit(&sm.sf_empty[sf.s]);
+          ring = nx;
+          sf = sn;
         }
         if (ok) ptx::mma_commit(&sm.tmem_full[acc]);
       }
@@ -286,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!SF_TMA) fetch(0);
       for (int kb = 0; kb < kbs; ++kb, ring.next(), sf.next()) {
         if (SF_TMA) {
-          if (!warp_wait<true>(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) {
+          if (!warp_wait(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) {
             ok = false;
             break;
           }
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             vb[j][0] = v.x, vb[j][1] = v.y, vb[j][2] = v.z, vb[j][3] = v.w;
           }
         }
-        if (!warp_wait<true>(&sm.sf_empty[sf.s], sf.ph ^ 1u, &sm.abort, p.status)) {
+        if (!warp_wait(&sm.sf_empty[sf.s], sf.ph ^ 1u, &sm.abort, p.status)) {
           ok = false;
           break;
         }
@@ -341,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = tl.blk * BM + q * 32 + lane;
       const bool live = n < p.N;
       const float wn = p.rw && live ? p.rw[(long)tl.e * p.N + n] : 1.0f;
-      if (!warp_wait<false>(&sm.tmem_full[acc], aph, &sm.abort, p.status)) break;
+      if (!warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status)) break;
       ptx::tc_fence_after();
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
 #pragma unroll 1
