@@ -7,7 +7,6 @@ no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from ctypes import POINTER, c_char_p, c_float, c_int, c_size_t, c_uint64, c_void_p
@@ -327,22 +326,34 @@ _TORCH_OUT = {"f32": torch.float32, "bf16": torch.bfloat16}
 _DTYPE_OF = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
-def _on(stream, first: torch.Tensor, *others: Optional[torch.Tensor]):
-    """The context to allocate and launch in: the device of the tensors (all on one)
-    and `stream`, so that what is allocated for the call belongs to the stream that uses it."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got one on {dev}")
+def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """The one CUDA device of the tensors."""
+    d = first.get_device()
+    if d < 0:
+        raise ValueError(f"expected CUDA tensors, got one on {first.device}")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-        return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
-        return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    return d
+
+
+def _elsewhere(d: int, stream) -> bool:
+    """Whether a call on device d and `stream` needs another context than the current one."""
+    return stream is not None or d != torch.cuda.current_device()
+
+
+def _on(d: int, stream):
+    """The context of device d and `stream`, so that what is allocated for a call belongs to
+    the stream that uses it."""
+    if stream is None:
+        return torch.cuda.device(d)
+    if stream.device.index != d:
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{d}")
+    return torch.cuda.stream(stream)
+
+
+def _raw_stream(d: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(d)
 
 
 def _act_dtype(t: torch.Tensor, what: str) -> int:
@@ -392,13 +403,16 @@ def grouped_matmul(a: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Ten
     odt = _TORCH_OUT[out] if out else (y.dtype if y is not None else a.dtype)
     g = MoEGrouped(E, rows, N, K, _act_dtype(a, "a"), _DTYPE_OF.get(odt, -1))
     _expect(y, (rows, N), odt, "y")
-    with _on(stream, a, w, offsets, row_weight, y, ws):
-        if y is None:
-            y = torch.empty((rows, N), dtype=odt, device=a.device)
-        if ws is None:
-            ws = workspace(256, a.device)
-        _check(lib.moe_grouped_matmul(ctypes.byref(g), _p(a), _p(offsets), _p(w), int(transposed), _p(row_weight),
-                                      _p(y), _p(ws), ws.numel(), _stream()), "moe_grouped_matmul")
+    d = _device(a, w, offsets, row_weight, y, ws)
+    if _elsewhere(d, stream):
+        with _on(d, stream):
+            return grouped_matmul(a, w, offsets, transposed, row_weight, y, out, ws)
+    if y is None:
+        y = torch.empty((rows, N), dtype=odt, device=a.device)
+    if ws is None:
+        ws = workspace(256, a.device)
+    _check(lib.moe_grouped_matmul(g, _p(a), _p(offsets), _p(w), transposed, _p(row_weight), _p(y), _p(ws), ws.numel(),
+                                  _raw_stream(d)), "moe_grouped_matmul")
     return y
 
 
@@ -420,13 +434,16 @@ def grouped_wgrad(dy: torch.Tensor, a: torch.Tensor, offsets: Optional[torch.Ten
     odt = _TORCH_OUT[out] if out else (dw.dtype if dw is not None else a.dtype)
     g = MoEGrouped(E, rows, N, K, _act_dtype(a, "a"), _DTYPE_OF.get(odt, -1))
     _expect(dw, (E, N, K), odt, "dw")
-    with _on(stream, a, dy, offsets, dw, ws):
-        if dw is None:
-            dw = torch.empty((E, N, K), dtype=odt, device=a.device)
-        if ws is None:
-            ws = workspace(256, a.device)
-        _check(lib.moe_grouped_wgrad(ctypes.byref(g), _p(dy), _p(a), _p(offsets), int(accumulate), _p(dw), _p(ws),
-                                     ws.numel(), _stream()), "moe_grouped_wgrad")
+    d = _device(a, dy, offsets, dw, ws)
+    if _elsewhere(d, stream):
+        with _on(d, stream):
+            return grouped_wgrad(dy, a, offsets, dw, accumulate, out, ws)
+    if dw is None:
+        dw = torch.empty((E, N, K), dtype=odt, device=a.device)
+    if ws is None:
+        ws = workspace(256, a.device)
+    _check(lib.moe_grouped_wgrad(g, _p(dy), _p(a), _p(offsets), accumulate, _p(dw), _p(ws), ws.numel(),
+                                 _raw_stream(d)), "moe_grouped_wgrad")
     return dw
 
 
@@ -450,14 +467,18 @@ def grouped_matmul_nvfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     odt = _TORCH_OUT[out] if out else (y.dtype if y is not None else torch.bfloat16)
     g = MoEGrouped(E, rows, N, K, MOE_NVFP4, _DTYPE_OF.get(odt, -1))
     _expect(y, (rows, N), odt, "y")
-    with _on(stream, a, a_scales, w, w_scales, offsets, a_row_scale, w_row_scale, row_weight, y, ws):
-        if y is None:
-            y = torch.empty((rows, N), dtype=odt, device=a.device)
-        if ws is None:
-            ws = workspace(256, a.device)
-        _check(lib.moe_grouped_matmul_nvfp4(ctypes.byref(g), _p(a), _p(a_scales), _p(a_row_scale), _p(offsets), _p(w),
-                                            _p(w_scales), _p(w_row_scale), _p(row_weight), _p(y), _p(ws), ws.numel(),
-                                            _stream()), "moe_grouped_matmul_nvfp4")
+    d = _device(a, a_scales, w, w_scales, offsets, a_row_scale, w_row_scale, row_weight, y, ws)
+    if _elsewhere(d, stream):
+        with _on(d, stream):
+            return grouped_matmul_nvfp4(a, a_scales, w, w_scales, offsets, a_row_scale, w_row_scale, row_weight, y, out,
+                                        ws)
+    if y is None:
+        y = torch.empty((rows, N), dtype=odt, device=a.device)
+    if ws is None:
+        ws = workspace(256, a.device)
+    _check(lib.moe_grouped_matmul_nvfp4(g, _p(a), _p(a_scales), _p(a_row_scale), _p(offsets), _p(w), _p(w_scales),
+                                        _p(w_row_scale), _p(row_weight), _p(y), _p(ws), ws.numel(), _raw_stream(d)),
+           "moe_grouped_matmul_nvfp4")
     return y
 
 
@@ -471,18 +492,21 @@ def _live(offsets: Optional[torch.Tensor]):
 
 
 def _nvfp4_outputs(rows: int, cols: int, dev, row_scaled: bool, values: bool, out) -> Dict[str, torch.Tensor]:
-    shapes = dict(codes=((rows, cols // 2), torch.uint8), scales=((rows, cols // 16), torch.uint8),
-                  row_scale=((rows,), torch.float32) if row_scaled else None,
-                  values=((rows, cols), torch.bfloat16) if values else None)
     if out is None:
-        return {k: None if s is None else torch.empty(s[0], dtype=s[1], device=dev) for k, s in shapes.items()}
-    for k, s in shapes.items():
-        if s is None:
-            if out.get(k) is not None:
-                raise ValueError(f"out has {k}, which this call does not write")
-            continue
-        _need(out.get(k), s[0], s[1], k)
-    return {k: out.get(k) for k in shapes}
+        u8 = torch.uint8
+        return dict(codes=torch.empty((rows, cols // 2), dtype=u8, device=dev),
+                    scales=torch.empty((rows, cols // 16), dtype=u8, device=dev),
+                    row_scale=torch.empty(rows, dtype=torch.float32, device=dev) if row_scaled else None,
+                    values=torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if values else None)
+    if (out.get("row_scale") is not None and not row_scaled) or (out.get("values") is not None and not values):
+        raise ValueError("out has a tensor that this call does not write")
+    _need(out.get("codes"), (rows, cols // 2), torch.uint8, "codes")
+    _need(out.get("scales"), (rows, cols // 16), torch.uint8, "scales")
+    if row_scaled:
+        _need(out.get("row_scale"), (rows,), torch.float32, "row_scale")
+    if values:
+        _need(out.get("values"), (rows, cols), torch.bfloat16, "values")
+    return {k: out.get(k) for k in ("codes", "scales", "row_scale", "values")}
 
 
 def quantize_nvfp4(x: torch.Tensor, row_token: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
@@ -499,12 +523,14 @@ def quantize_nvfp4(x: torch.Tensor, row_token: Optional[torch.Tensor] = None, of
     if row_token is not None:
         rows = row_token.numel()
         _expect(row_token, (rows,), torch.int32, "row_token")
-    o = out or {}
-    with _on(stream, x, row_token, offsets, *[t for t in o.values() if t is not None]):
-        o = _nvfp4_outputs(rows, cols, x.device, row_scaled, values, out)
-        _check(lib.moe_quantize_nvfp4(rows, cols, dt, _p(x), x_rows, _p(row_token), _live(offsets), _p(o["codes"]),
-                                      _p(o["scales"]), _p(o["row_scale"]), _p(o["values"]), _stream()),
-               "moe_quantize_nvfp4")
+    d = _device(x, row_token, offsets, *(out.values() if out else ()))
+    if _elsewhere(d, stream):
+        with _on(d, stream):
+            return quantize_nvfp4(x, row_token, offsets, row_scaled, values, out)
+    o = _nvfp4_outputs(rows, cols, x.device, row_scaled, values, out)
+    _check(lib.moe_quantize_nvfp4(rows, cols, dt, _p(x), x_rows, _p(row_token), _live(offsets), _p(o["codes"]),
+                                  _p(o["scales"]), _p(o["row_scale"]), _p(o["values"]), _raw_stream(d)),
+           "moe_quantize_nvfp4")
     return o
 
 
@@ -521,12 +547,14 @@ def swiglu_quantize_nvfp4(gu: torch.Tensor, clamp: float = 0.0, clamp_mode="prea
                           stream=None) -> Dict[str, Optional[torch.Tensor]]:
     """quantize_nvfp4(swiglu(gu)) in one pass over gu [rows, 2 cols]."""
     rows, cols, dt = _gate_up(gu)
-    o = out or {}
-    with _on(stream, gu, offsets, *[t for t in o.values() if t is not None]):
-        o = _nvfp4_outputs(rows, cols, gu.device, row_scaled, values, out)
-        _check(lib.moe_swiglu_quantize_nvfp4(rows, cols, dt, _p(gu), clamp, CLAMP_MODES[clamp_mode], _live(offsets),
-                                             _p(o["codes"]), _p(o["scales"]), _p(o["row_scale"]), _p(o["values"]),
-                                             _stream()), "moe_swiglu_quantize_nvfp4")
+    d = _device(gu, offsets, *(out.values() if out else ()))
+    if _elsewhere(d, stream):
+        with _on(d, stream):
+            return swiglu_quantize_nvfp4(gu, clamp, clamp_mode, offsets, row_scaled, values, out)
+    o = _nvfp4_outputs(rows, cols, gu.device, row_scaled, values, out)
+    _check(lib.moe_swiglu_quantize_nvfp4(rows, cols, dt, _p(gu), clamp, CLAMP_MODES[clamp_mode], _live(offsets),
+                                         _p(o["codes"]), _p(o["scales"]), _p(o["row_scale"]), _p(o["values"]),
+                                         _raw_stream(d)), "moe_swiglu_quantize_nvfp4")
     return o
 
 
@@ -535,11 +563,14 @@ def swiglu(gu: torch.Tensor, clamp: float = 0.0, clamp_mode="preact", offsets: O
     """h = SiLU(g) u of gu [rows, 2F] = (g | u).  With offsets only the rows below its last entry."""
     rows, F, dt = _gate_up(gu)
     _expect(h, (rows, F), gu.dtype, "h")
-    with _on(stream, gu, offsets, h):
-        if h is None:
-            h = torch.empty((rows, F), dtype=gu.dtype, device=gu.device)
-        _check(lib.moe_swiglu(rows, F, dt, _p(gu), clamp, CLAMP_MODES[clamp_mode], _live(offsets), _p(h), _stream()),
-               "moe_swiglu")
+    d = _device(gu, offsets, h)
+    if _elsewhere(d, stream):
+        with _on(d, stream):
+            return swiglu(gu, clamp, clamp_mode, offsets, h)
+    if h is None:
+        h = torch.empty((rows, F), dtype=gu.dtype, device=gu.device)
+    _check(lib.moe_swiglu(rows, F, dt, _p(gu), clamp, CLAMP_MODES[clamp_mode], _live(offsets), _p(h), _raw_stream(d)),
+           "moe_swiglu")
     return h
 
 
@@ -553,21 +584,26 @@ def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, row_weight: Optional[tor
     rows, F, dt = _gate_up(gu)
     _need(dh, (rows, F), gu.dtype, "dh")
     _expect(row_weight, (rows,), torch.float32, "row_weight")
-    shapes = dict(dgu=((rows, 2 * F), gu.dtype), hw=((rows, F), gu.dtype) if need_hw else None,
-                  drow_weight=((rows,), torch.float32) if need_drow_weight else None)
     o = out or {}
-    for k, s in shapes.items():
-        if o.get(k) is not None:
-            if s is None:
-                raise ValueError(f"out has {k}, which this call does not write")
-            _expect(o[k], s[0], s[1], k)
-    with _on(stream, gu, dh, row_weight, offsets, *[t for t in o.values() if t is not None]):
-        r = {k: o.get(k) if o.get(k) is not None or s is None else torch.empty(s[0], dtype=s[1], device=gu.device)
-             for k, s in shapes.items()}
-        _check(lib.moe_swiglu_backward(rows, F, dt, _p(gu), _p(dh), _p(row_weight), clamp, CLAMP_MODES[clamp_mode],
-                                       _live(offsets), _p(r["dgu"]), _p(r["hw"]), _p(r["drow_weight"]), _stream()),
-               "moe_swiglu_backward")
-    return r
+    dgu, hw, drw = o.get("dgu"), o.get("hw"), o.get("drow_weight")
+    if (hw is not None and not need_hw) or (drw is not None and not need_drow_weight):
+        raise ValueError("out has a tensor that this call does not write")
+    _expect(dgu, (rows, 2 * F), gu.dtype, "dgu")
+    _expect(hw, (rows, F), gu.dtype, "hw")
+    _expect(drw, (rows,), torch.float32, "drow_weight")
+    d = _device(gu, dh, row_weight, offsets, dgu, hw, drw)
+    if _elsewhere(d, stream):
+        with _on(d, stream):
+            return swiglu_backward(gu, dh, row_weight, clamp, clamp_mode, offsets, need_hw, need_drow_weight, out)
+    if dgu is None:
+        dgu = torch.empty_like(gu)
+    if hw is None and need_hw:
+        hw = torch.empty_like(dh)
+    if drw is None and need_drow_weight:
+        drw = torch.empty(rows, dtype=torch.float32, device=gu.device)
+    _check(lib.moe_swiglu_backward(rows, F, dt, _p(gu), _p(dh), _p(row_weight), clamp, CLAMP_MODES[clamp_mode],
+                                   _live(offsets), _p(dgu), _p(hw), _p(drw), _raw_stream(d)), "moe_swiglu_backward")
+    return dict(dgu=dgu, hw=hw, drow_weight=drw)
 
 
 STAGES = ("route", "dispatch", "gate_up", "down", "shared", "combine")

@@ -30,7 +30,7 @@
 //             two accumulators let the epilogue of tile i overlap the MMAs
 //             of tile i+1
 //   warps 2-5 epilogue: TMEM lane = output feature
-//   warp 6    TN: clears the lines above and hands every stage on to the MMAs
+//   warp 6    TN: clears the lines above and hands the stage on to the MMAs
 //
 // Every wait is bounded (2 s, then MOE_ERR_DEVICE_TIMEOUT in the status word
 // and an orderly wind down).
@@ -58,12 +58,18 @@ constexpr int A_BYTES = BM * BK * 2;  // 16 KB
 constexpr int BOX = 64 * BK * 2;     // 8 KB: an MN-major box
 
 // BT: tokens (NT, NN) or columns (TN) per tile, the MMA's largest N.
+// Pairs (BT = 256): a tile has 256 output features, 128 a CTA of a 2-CTA
+// cluster; each CTA stages its own features and half of the tokens.
 template <int BT>
 struct Cfg {
-  static constexpr int B_BYTES = BT * BK * 2;
+  static constexpr bool PAIR = BT == 256;
+  static constexpr int TILE_M = PAIR ? 2 * BM : BM;
+  static constexpr int B_ROWS = PAIR ? BT / 2 : BT;  // staged by one CTA
+  static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BT == 256 ? 4 : 8;
-  static constexpr int TOK_BOX = BT == 256 ? 64 : 32;  // token rows per TMA box (NT, NN)
+  static constexpr int STAGES = PAIR ? 6 : 8;
+  static constexpr int TOK_BOX = PAIR ? 64 : 32;     // token rows per TMA box (NT, NN)
+  static constexpr int N_STEP = PAIR ? 32 : 16;      // N of the MMAs is a multiple of it
   static constexpr uint32_t TMEM_COLS = 2 * BT;
 };
 template <Mode MODE>
@@ -73,7 +79,8 @@ constexpr int kClearWarp = 6;  // TN
 template <int STAGES>
 struct Smem {
   uint64_t full[STAGES];    // stage ready for the MMAs
-  uint64_t landed[STAGES];  // TN: its copies are complete
+  uint64_t landed[STAGES];  // TN: the copies of a last, partial block are complete in this CTA
+  uint64_t cleared[STAGES]; // TN, leader: and the peer has cleared its lines
   uint64_t empty[STAGES];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
@@ -88,7 +95,7 @@ static_assert(sizeof(Smem<8>) <= kSmemPart, "the epilogue staging follows the ba
 
 struct Params {
   int rows, N, K, E;
-  int m_blocks;    // 128-feature blocks of the output
+  int m_blocks;    // TILE_M-feature blocks of the output
   int n_blocks;    // TN: BT-column blocks
   const int32_t *offsets;
   const float *row_weight;
@@ -97,6 +104,12 @@ struct Params {
   int accumulate;  // TN
   int *status;
 };
+
+__device__ __forceinline__ void spin_ns(uint64_t ns) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (ptx::globaltimer_ns() - t0 < ns) {
+  }
+}
 
 // Shared-memory descriptor of an MN-major tile with the 128-byte swizzle:
 // boxes of 64 features (128 bytes) x 64 reduction elements; leading byte
@@ -124,17 +137,23 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   Smem<STAGES> &sm = *reinterpret_cast<Smem<STAGES> *>(base + STAGES * C::STAGE_BYTES);
   uint32_t *staging = reinterpret_cast<uint32_t *>(base + STAGES * C::STAGE_BYTES + kSmemPart);
 
+  constexpr bool PAIR = C::PAIR;
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+  const int unit = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int n_units = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       ptx::mbar_init(&sm.full[s], 1);
+      ptx::mbar_init(&sm.cleared[s], 1);
       ptx::mbar_init(&sm.landed[s], 1);
       ptx::mbar_init(&sm.empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&sm.tmem_full[a], 1);
-      ptx::mbar_init(&sm.tmem_empty[a], 4);
+      ptx::mbar_init(&sm.tmem_empty[a], PAIR ? 8 : 4);  // epilogue warps
     }
     ptx::mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -146,8 +165,13 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     ptx::prefetch_tmap(&tmB);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(&sm.tmem_base, C::TMEM_COLS);
-    ptx::tmem_relinquish();
+    if (PAIR) {
+      ptx::tmem_alloc_pair(&sm.tmem_base, C::TMEM_COLS);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(&sm.tmem_base, C::TMEM_COLS);
+      ptx::tmem_relinquish();
+    }
   }
   if (warp == 2) {
     // TN needs no tile list (every group has m_blocks * n_blocks tiles), but
@@ -157,7 +181,9 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     if (kChecked && MODE == TN && lane == 0) sm.start[0] = ok ? 0 : 1;
   }
   ptx::tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if (PAIR) ptx::cluster_sync();  // the peer's copies and arrivals may reach this CTA's barriers from here on
+  else __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = sm.tmem_base;
   int total;
@@ -167,6 +193,9 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   // tile t -> group, feature block, first row / column, reduction blocks
   struct Tile {
     int e, m0, c0, count, row0, red;  // c0: first column (TN); count: tokens or columns; red: reduction length
+    // MMA N, and the tokens or columns that this CTA stages of it
+    __device__ int width() const { return (count + C::N_STEP - 1) & ~(C::N_STEP - 1); }
+    __device__ int staged() const { return PAIR ? width() / 2 : width(); }
   };
   auto tile_of = [&](int t) {
     Tile r;
@@ -175,16 +204,16 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       r.e = t / per;
       const int local = t - r.e * per;
       const int nb = local / p.m_blocks;
-      r.m0 = (local - nb * p.m_blocks) * BM;
+      r.m0 = (local - nb * p.m_blocks) * C::TILE_M;
       r.c0 = nb * BT;
       r.count = p.K - r.c0 < BT ? p.K - r.c0 : BT;
       r.row0 = seg_begin(p.offsets, p.rows, r.e);
       r.red = seg_end(p.offsets, p.rows, r.e) - r.row0;
       if (r.red < 0) r.red = 0;
     } else {
-      const TokenTile tt = token_tile(sm.start, p.offsets, p.rows, p.E, p.m_blocks, t);
+      const TokenTile tt = token_tile(sm.start, p.offsets, p.rows, p.E, p.m_blocks, t, C::N_STEP);
       r.e = tt.e;
-      r.m0 = tt.blk * BM;
+      r.m0 = tt.blk * C::TILE_M;
       r.c0 = 0;
       r.row0 = tt.row0;
       r.count = tt.count;
@@ -196,54 +225,85 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   if (warp == 0) {
     // ================================================= TMA producer
     if (elect_one()) {
-      uint64_t *const bars = MODE == TN ? sm.landed : sm.full;
+      uint32_t used = 0, phase = 0;  // TN: stages whose landed barrier was used, and its next phase
       Ring<STAGES> ring;
       uint32_t issued = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      for (int t = unit; t < total && ok; t += n_units) {
         const Tile tl = tile_of(t);
         const int kbs = (tl.red + BK - 1) / BK;
-        const int boxes = MODE == TN ? (tl.count + 63) / 64 : (tl.count + C::TOK_BOX - 1) / C::TOK_BOX;
+        const int staged = tl.staged();
+        const int boxes = MODE == TN ? (staged + 63) / 64 : (staged + C::TOK_BOX - 1) / C::TOK_BOX;
         const uint32_t tx = A_BYTES + (uint32_t)boxes * (MODE == TN ? BOX : C::TOK_BOX * BK * 2);
+        const int m0 = tl.m0 + (int)rank * BM;                                    // this CTA's features
+        const int b0 = (MODE == TN ? tl.c0 : tl.row0) + (int)rank * staged;       // and columns or tokens
         for (int kb = 0; kb < kbs; ++kb, ring.next(), ++issued) {
           if (!wait_bar(&sm.empty[ring.s], ring.ph ^ 1u, &sm.abort, p.status)) {
             ok = false;
             break;
           }
-          uint64_t *bar = &bars[ring.s];
+          uint64_t *bar = &sm.full[ring.s];
           uint8_t *a = stage_a + ring.s * A_BYTES;
           uint8_t *b = stage_b + ring.s * C::B_BYTES;
           const int k0 = kb * BK;
+          const bool partial = MODE == TN && tl.red - k0 < BK;
+          if (PAIR && !partial) {
+            // both CTAs' copies complete on the leader's barrier
+            const uint32_t lead = ptx::map_to_rank(bar, 0);
+            if (rank == 0) ptx::mbar_arrive_expect_tx(bar, 2 * tx);
+            if (MODE == NT) {
+              ptx::tma_load_3d_pair(a, &tmA, lead, k0, m0, tl.e);
+            } else if (MODE == NN) {
+              ptx::tma_load_3d_pair(a, &tmA, lead, m0, k0, tl.e);
+              ptx::tma_load_3d_pair(a + BOX, &tmA, lead, m0 + 64, k0, tl.e);
+            } else {
+              ptx::tma_load_2d_pair(a, &tmA, lead, m0, tl.row0 + k0);
+              ptx::tma_load_2d_pair(a + BOX, &tmA, lead, m0 + 64, tl.row0 + k0);
+            }
+            for (int i = 0; i < boxes; ++i) {
+              if (MODE == TN) ptx::tma_load_2d_pair(b + i * BOX, &tmB, lead, b0 + i * 64, tl.row0 + k0);
+              else ptx::tma_load_2d_pair(b + i * C::TOK_BOX * BK * 2, &tmB, lead, k0, b0 + i * C::TOK_BOX);
+            }
+            continue;
+          }
+          if (MODE == TN) {  // the clearing warp hands the stage on
+            bar = &sm.landed[ring.s];
+            used |= 1u << ring.s;
+            phase ^= 1u << ring.s;
+          }
           ptx::mbar_arrive_expect_tx(bar, tx);
           if (MODE == NT) {
-            ptx::tma_load_3d(a, &tmA, bar, k0, tl.m0, tl.e);
+            ptx::tma_load_3d(a, &tmA, bar, k0, m0, tl.e);
           } else if (MODE == NN) {
-            ptx::tma_load_3d(a, &tmA, bar, tl.m0, k0, tl.e);
-            ptx::tma_load_3d(a + BOX, &tmA, bar, tl.m0 + 64, k0, tl.e);
+            ptx::tma_load_3d(a, &tmA, bar, m0, k0, tl.e);
+            ptx::tma_load_3d(a + BOX, &tmA, bar, m0 + 64, k0, tl.e);
           } else {
-            ptx::tma_load_2d(a, &tmA, bar, tl.m0, tl.row0 + k0);
-            ptx::tma_load_2d(a + BOX, &tmA, bar, tl.m0 + 64, tl.row0 + k0);
+            ptx::tma_load_2d(a, &tmA, bar, m0, tl.row0 + k0);
+            ptx::tma_load_2d(a + BOX, &tmA, bar, m0 + 64, tl.row0 + k0);
           }
           for (int i = 0; i < boxes; ++i) {
-            if (MODE == TN) ptx::tma_load_2d(b + i * BOX, &tmB, bar, tl.c0 + i * 64, tl.row0 + k0);
-            else ptx::tma_load_2d(b + i * C::TOK_BOX * BK * 2, &tmB, bar, k0, tl.row0 + i * C::TOK_BOX);
+            if (MODE == TN) ptx::tma_load_2d(b + i * BOX, &tmB, bar, b0 + i * 64, tl.row0 + k0);
+            else ptx::tma_load_2d(b + i * C::TOK_BOX * BK * 2, &tmB, bar, k0, b0 + i * C::TOK_BOX);
           }
         }
       }
-      // every issued copy has landed before shared memory is released
+      // every issued copy has landed before shared memory is released (a peer's
+      // complete on the leader's barriers, which the leader waits for)
       for (int s = 0; s < STAGES; ++s) {
-        if ((uint32_t)s >= issued) break;
+        if (MODE == TN && (used >> s & 1)) drain_bar(&sm.landed[s], (phase >> s & 1) ^ 1u, p.status);
+        if (rank != 0 || (uint32_t)s >= issued) continue;
         const uint32_t last = (issued - 1 - s) / STAGES;  // this stage's last round
-        drain_bar(&bars[s], last & 1u, p.status);
+        drain_bar(&sm.full[s], last & 1u, p.status);
       }
+      if (rank != 0 && !ok) spin_ns(1000000);  // an aborting peer gives its last copies time to land
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ================================================= MMA issuer
-    if (elect_one()) {
+    // ================================================= MMA issuer (a pair's leader)
+    if (rank == 0 && elect_one()) {
       // D fp32, A and B bf16; bit 15: A is MN-major, bit 16: B is
       constexpr uint32_t idesc0 =
-          ptx::idesc_bf16_f32(BM, 0) | (MODE != NT ? 1u << 15 : 0u) | (MODE == TN ? 1u << 16 : 0u);
+          ptx::idesc_bf16_f32(C::TILE_M, 0) | (MODE != NT ? 1u << 15 : 0u) | (MODE == TN ? 1u << 16 : 0u);
       // descriptors of stage 0; an address moves by its bytes >> 4
       const uint64_t ad0 = MODE == NT ? ptx::desc_kmajor_sw128(ptx::smem_addr(stage_a))
                                       : desc_mnmajor_sw128(ptx::smem_addr(stage_a));
@@ -251,11 +311,19 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
                                       : ptx::desc_kmajor_sw128(ptx::smem_addr(stage_b));
       constexpr uint32_t a_step = (MODE == NT ? UMMA_K * 2 : UMMA_K * 128) >> 4;
       constexpr uint32_t b_step = (MODE == TN ? UMMA_K * 128 : UMMA_K * 2) >> 4;
+      auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+        if (PAIR) ptx::mma_bf16_pair(d, a, b, id, acc);
+        else ptx::mma_bf16(d, a, b, id, acc);
+      };
+      auto commit = [](uint64_t *bar) {  // pairs: on both CTAs' barriers
+        if (PAIR) ptx::mma_commit_pair_mc(bar, 0x3);
+        else ptx::mma_commit(bar);
+      };
       Ring<STAGES> ring;
       bool ready = false;  // the next stage's barrier, read ahead of the MMAs before it
       int i = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      for (int t = unit; t < total && ok; t += n_units) {
         const Tile tl = tile_of(t);
         const int kbs = (tl.red + BK - 1) / BK;
         if (kbs == 0) continue;  // TN, empty group: the epilogue needs no sum
@@ -265,7 +333,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
         if (!wait_bar(&sm.tmem_empty[acc], aph ^ 1u, &sm.abort, p.status)) break;
         ptx::tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BT;
-        const uint32_t idesc = idesc0 | (uint32_t)((tl.count + 15) >> 4) << 18;  // N >> 3 at bit 17, N a multiple of 16
+        const uint32_t idesc = idesc0 | (uint32_t)(tl.width() >> 3) << 17;
         for (int kb = 0; kb < kbs; ++kb) {
           if (!ready && !wait_bar(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) {
             ok = false;
@@ -280,56 +348,59 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
           if (MODE == TN && left <= BK - UMMA_K) {
             const int steps = (left + UMMA_K - 1) / UMMA_K;
             for (int k = 0; k < steps; ++k)
-              ptx::mma_bf16(d_tmem, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
+              mma(d_tmem, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
           } else {
 #pragma unroll
             for (int k = 0; k < BK / UMMA_K; ++k)
-              ptx::mma_bf16(d_tmem, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
+              mma(d_tmem, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
           }
-          ptx::mma_commit(&sm.empty[ring.s]);
+          commit(&sm.empty[ring.s]);
           ring = nx;
         }
-        if (ok) ptx::mma_commit(&sm.tmem_full[acc]);
+        if (ok) commit(&sm.tmem_full[acc]);
       }
       // all issued MMAs complete before TMEM is released
-      ptx::mma_commit(&sm.drain);
+      if (PAIR) ptx::mma_commit_pair(&sm.drain);
+      else ptx::mma_commit(&sm.drain);
       drain_bar(&sm.drain, 0, p.status);
     }
     __syncwarp();
   } else if (MODE == TN && warp == kClearWarp) {
     // ================================================= lines of other rows (TN)
-    Ring<STAGES> ring;
-    bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    uint32_t at = 0, phase = 0;  // blocks so far; next phase of each stage's landed barrier
+    for (int t = unit; t < total; t += n_units) {
       const Tile tl = tile_of(t);
-      const int kbs = (tl.red + BK - 1) / BK;
-      const int boxes = (tl.count + 63) / 64;
-      for (int kb = 0; kb < kbs; ++kb, ring.next()) {
-        if (!warp_wait(&sm.landed[ring.s], ring.ph, &sm.abort, p.status)) {
-          ok = false;
-          break;
-        }
-        const int left = tl.red - kb * BK;
-        if (left < BK) {  // lines [left, the MMAs' last) of every box
-          uint8_t *a = stage_a + ring.s * A_BYTES, *b = stage_b + ring.s * C::B_BYTES;
-          const int pieces = (((left + UMMA_K - 1) & ~(UMMA_K - 1)) - left) * 8;  // of 16 bytes, a box
-          for (int j = lane; j < pieces * (2 + boxes); j += 32) {
-            const int box = j / pieces, in = j - box * pieces;
-            uint8_t *q = (box < 2 ? a + box * BOX : b + (box - 2) * BOX) + left * 128 + in * 16;
-            *reinterpret_cast<uint4 *>(q) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.full[ring.s]);
+      const int left = tl.red % BK;
+      at += (tl.red + BK - 1) / BK;
+      if (left == 0) continue;
+      const int s = (at - 1) % STAGES;
+      if (!warp_wait(&sm.landed[s], phase >> s & 1, &sm.abort, p.status)) break;
+      __syncwarp();
+      // lines [left, the MMAs' last) of every box
+      uint8_t *a = stage_a + s * A_BYTES, *b = stage_b + s * C::B_BYTES;
+      const int boxes = (tl.staged() + 63) / 64;
+      const int pieces = (((left + UMMA_K - 1) & ~(UMMA_K - 1)) - left) * 8;  // of 16 bytes, a box
+      for (int j = lane; j < pieces * (2 + boxes); j += 32) {
+        const int box = j / pieces, in = j - box * pieces;
+        uint8_t *q = (box < 2 ? a + box * BOX : b + (box - 2) * BOX) + left * 128 + in * 16;
+        *reinterpret_cast<uint4 *>(q) = make_uint4(0, 0, 0, 0);
       }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (rank != 0) {
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(&sm.cleared[s], 0));
+      } else {
+        if (!warp_wait(&sm.cleared[s], phase >> s & 1, &sm.abort, p.status)) break;
+        if (lane == 0) ptx::mbar_arrive(&sm.full[s]);
+      }
+      phase ^= 1u << s;
     }
   } else {
     // ================================================= epilogue (warps 2..5)
     const int q = warp & 3;  // TMEM lane quadrant this warp may access
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
     int i = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    for (int t = unit; t < total; t += n_units) {
       const Tile tl = tile_of(t);
       const bool have = MODE != TN || tl.red > 0;
       const int acc = i & 1;
@@ -341,7 +412,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       }
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
       if (MODE != TN) {
-        const int n = tl.m0 + q * 32 + lane;
+        const int n = tl.m0 + (int)rank * BM + q * 32 + lane;
         const bool live = n < p.N;
 #pragma unroll 1
         for (int c = 0; c < tl.count; c += 32) {
@@ -377,7 +448,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
         // warp's 4 KB (16-byte piece j of row r at j ^ (r % 8)), so that every
         // store writes four whole 128-byte row segments
         uint32_t *stg = staging + q * 32 * 32;
-        const int n_first = tl.m0 + q * 32;
+        const int n_first = tl.m0 + (int)rank * BM + q * 32;
         const int rr = lane >> 3, ff = lane & 7;
         // words staged as fp32 sums, or as bf16 pairs already rounded (bf16
         // out without a previous value to add: the sum is rounded once either way)
@@ -449,18 +520,23 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       if (have) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.tmem_empty[acc]);
+        if (lane == 0) {
+          if (PAIR) ptx::mbar_arrive_cluster(ptx::map_to_rank(&sm.tmem_empty[acc], 0));
+          else ptx::mbar_arrive(&sm.tmem_empty[acc]);
+        }
       }
     }
   }
 
   ptx::tc_fence_before();
   __syncwarp();
-  __syncthreads();
+  if (PAIR) ptx::cluster_sync();  // neither CTA leaves while the pair's copies, MMAs or arrivals are pending
+  else __syncthreads();
   if (warp == 1) {
     __syncwarp();
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem_base, C::TMEM_COLS);
+    if (PAIR) ptx::tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else ptx::tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
 }
 
@@ -480,10 +556,7 @@ moe_status launch(Params &p, const void *a, const void *b, cudaStream_t s) {
          tma_map_bf16(&tb, b, 2, (uint64_t)p.K, (uint64_t)p.rows, 1, BK);
   }
   if (!ok) return MOE_ERR_CUDA;
-  int dev = 0, sms = 148;
-  MOE_CUDA_TRY(cudaGetDevice(&dev));
-  MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  p.m_blocks = (p.N + BM - 1) / BM;
+  p.m_blocks = (p.N + C::TILE_M - 1) / C::TILE_M;
   p.n_blocks = (p.K + BT - 1) / BT;
   const long used = p.rows < p.E ? p.rows : p.E;  // groups with rows
   const long tiles = MODE == TN ? (long)p.E * p.m_blocks * p.n_blocks
@@ -491,8 +564,27 @@ moe_status launch(Params &p, const void *a, const void *b, cudaStream_t s) {
   if (tiles > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
   const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart + (MODE == TN ? kStaging : 0);
   auto kern = grouped_gemm<MODE, BT>;
-  MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  kern<<<(int)(tiles < sms ? tiles : sms), kThreads<MODE>, smem, s>>>(ta, tb, p);
+  static std::atomic<uint64_t> known[kMaxDevices];
+  Launch l;
+  const moe_status st = prepare_launch(kern, kThreads<MODE>, smem, C::PAIR, known, l);
+  if (st != MOE_OK) return st;
+  if (!C::PAIR) {
+    kern<<<(int)(tiles < l.sms ? tiles : l.sms), kThreads<MODE>, smem, s>>>(ta, tb, p);
+  } else {
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    lc.gridDim = dim3((unsigned)(2 * (tiles < l.pairs ? tiles : l.pairs)));
+    lc.blockDim = dim3(kThreads<MODE>);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = s;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    MOE_CUDA_TRY(cudaLaunchKernelEx(&lc, kern, ta, tb, p));
+  }
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = sm.tmem_base;
   const int total = sm.start[p.E] * p.m_blocks;
   const int kbs = (p.K + BK - 1) / BK;
-  auto tile_of = [&](int t) { return token_tile(sm.start, p.offsets, p.rows, p.E, p.m_blocks, t); };
+  auto tile_of = [&](int t) { return token_tile(sm.start, p.offsets, p.rows, p.E, p.m_blocks, t, 16); };
 
   if (warp == 0) {
     // ================================================= TMA producer
@@ -415,17 +415,17 @@ moe_status launch(Params &p, const void *a, const void *w, cudaStream_t s) {
   if (SF_TMA && (!tma_map_u8(&tsa, p.sw, (uint64_t)p.K / 16, p.N, p.E, 16, BM) ||
                  !tma_map_u8(&tsb, p.sa, (uint64_t)p.K / 16, p.rows, 1, 16, TOK_BOX)))
     return MOE_ERR_CUDA;
-  int dev = 0, sms = 148;
-  MOE_CUDA_TRY(cudaGetDevice(&dev));
-  MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   p.m_blocks = (p.N + BM - 1) / BM;
   const long used = p.rows < p.E ? p.rows : p.E;
   const long tiles = ((long)(p.rows + BT - 1) / BT + used) * p.m_blocks;
   if (tiles > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
   const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart;
   auto kern = grouped_gemm_fp4<BT, SF_TMA>;
-  MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  kern<<<(int)(tiles < sms ? tiles : sms), kThreads, smem, s>>>(ta, tb, tsa, tsb, p);
+  static std::atomic<uint64_t> known[kMaxDevices];
+  Launch l;
+  const moe_status st = prepare_launch(kern, kThreads, smem, false, known, l);
+  if (st != MOE_OK) return st;
+  kern<<<(int)(tiles < l.sms ? tiles : l.sms), kThreads, smem, s>>>(ta, tb, tsa, tsb, p);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }

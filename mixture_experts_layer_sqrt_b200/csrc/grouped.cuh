@@ -3,6 +3,8 @@
 // the rows of a group.  Internal to libmoe_b200.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "tc_ptx.cuh"
 
@@ -63,6 +65,47 @@ __device__ __forceinline__ void drain_bar(uint64_t *bar, uint32_t parity, int *s
       return;
     }
   }
+}
+
+// Per device and kernel, asked for once (host): the SM count, room for the
+// kernel's dynamic shared memory, and the 2-CTA clusters that are resident at
+// once (0 for kernels without clusters).  These calls and the tensor maps were
+// most of the host time of a small product.
+constexpr int kMaxDevices = 64;
+struct Launch {
+  int sms = 0, pairs = 0;
+};
+template <typename K>
+inline moe_status prepare_launch(K kern, int threads, size_t smem, bool pair, std::atomic<uint64_t> (&known)[kMaxDevices],
+                                 Launch &l) {
+  int dev = 0;
+  MOE_CUDA_TRY(cudaGetDevice(&dev));
+  const bool cached = dev >= 0 && dev < kMaxDevices;
+  uint64_t v = cached ? known[dev].load(std::memory_order_acquire) : 0;
+  if (!v) {
+    int sms = 0, pairs = 0;
+    MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    if (pair) {
+      cudaLaunchConfig_t lc = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      lc.gridDim = dim3(2);
+      lc.blockDim = dim3(threads);
+      lc.dynamicSmemBytes = smem;
+      lc.attrs = attr;
+      lc.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&pairs, kern, &lc) != cudaSuccess || pairs <= 0) pairs = sms / 2;
+    }
+    v = ((uint64_t)pairs << 32) | (uint32_t)sms;
+    if (cached) known[dev].store(v, std::memory_order_release);
+  }
+  l.sms = (int)(uint32_t)v;
+  l.pairs = (int)(v >> 32);
+  return MOE_OK;
 }
 
 // Place in a ring of N stages: the stage and the parity of its current round.
@@ -134,13 +177,14 @@ __device__ __forceinline__ int find_group(const int *start, int E, int per, int 
 }
 
 // A tile of tokens: group e's rows are cut into as few tiles of at most
-// tile_rows as hold them, of nearly equal widths (multiples of 16, the MMA's
-// N step), so that 300 rows are 160 + 140 and not 256 + 44.
+// tile_rows as hold them, of nearly equal widths (multiples of `step`, that of
+// the MMA's N), so that 300 rows are 160 + 140 and not 256 + 44: the copies of
+// a narrow tile's weights would outlast its MMAs.
 struct TokenTile {
   int e, blk, row0, count;  // group, output-feature block, first row, rows
 };
 __device__ __forceinline__ TokenTile token_tile(const int *start, const int32_t *offsets, int rows, int E, int blocks,
-                                                int t) {
+                                                int t, int step) {
   TokenTile r;
   r.e = find_group(start, E, blocks, t);
   const int tiles = start[r.e + 1] - start[r.e];
@@ -148,7 +192,7 @@ __device__ __forceinline__ TokenTile token_tile(const int *start, const int32_t 
   r.blk = local / tiles;
   const int j = local - r.blk * tiles;
   const int begin = seg_begin(offsets, rows, r.e), end = seg_end(offsets, rows, r.e);
-  const int width = ((end - begin + tiles - 1) / tiles + 15) & ~15;
+  const int width = ((end - begin + tiles - 1) / tiles + step - 1) & ~(step - 1);
   r.row0 = begin + j * width;
   r.count = end - r.row0 < width ? end - r.row0 : width;
   return r;
