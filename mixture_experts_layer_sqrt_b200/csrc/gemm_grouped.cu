@@ -85,12 +85,14 @@ struct Smem {
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint64_t drain;
+  __align__(16) float wbuf[4 * 32];  // row factors, 32 an epilogue warp
   uint32_t tmem_base;
   int abort;
   int start[MAX_E + 1];
 };
-constexpr int kSmemPart = 4608;                 // barriers and tile list
-constexpr int kStaging = 4 * 32 * 32 * 4;       // TN epilogue: 4 KB per warp
+constexpr int kSmemPart = 5120;             // barriers and tile list
+constexpr int kStaging = 4 * 32 * 32 * 4;   // epilogue: 4 KB a warp (TN), or two buffers of 32 tokens
+static_assert(kStaging == kRowStage, "one size for both epilogues");
 static_assert(sizeof(Smem<8>) <= kSmemPart, "the epilogue staging follows the barriers and tile list");
 
 struct Params {
@@ -399,6 +401,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     // ================================================= epilogue (warps 2..5)
     const int q = warp & 3;  // TMEM lane quadrant this warp may access
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    const RowStore store = {p.out, p.out_f32, p.N, p.row_weight, nullptr};
     int i = 0;
     for (int t = unit; t < total; t += n_units) {
       const Tile tl = tile_of(t);
@@ -407,114 +410,114 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       const uint32_t aph = (i >> 1) & 1u;
       if (have) {
         ++i;
-        if (!warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status)) break;
+        if (!epi_all(warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status))) break;
         ptx::tc_fence_after();
       }
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
       if (MODE != TN) {
-        const int n = tl.m0 + (int)rank * BM + q * 32 + lane;
-        const bool live = n < p.N;
-#pragma unroll 1
-        for (int c = 0; c < tl.count; c += 32) {
-          uint32_t v[32];
-          ptx::tmem_ld32(tbase + c, v);
-          const float rw = p.row_weight && c + lane < tl.count ? p.row_weight[tl.row0 + c + lane] : 1.0f;
-          ptx::tmem_ld_wait();
-          const int left = tl.count - c;
-          if (p.out_f32) {
-            float *y = (float *)p.out + (long)(tl.row0 + c) * p.N + n;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float w = __shfl_sync(0xffffffffu, rw, j);
-              if (live && j < left) y[(long)j * p.N] = __uint_as_float(v[j]) * w;
-            }
-          } else {
-            // two tokens at a time: the even lane takes features (n, n+1) of
-            // the first, the odd lane (n-1, n) of the second
-            const int odd = lane & 1;
-            __nv_bfloat16 *y = (__nv_bfloat16 *)p.out + (long)(tl.row0 + c + odd) * p.N + (n - odd);
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float v0 = __uint_as_float(v[j]) * __shfl_sync(0xffffffffu, rw, j);
-              const float v1 = __uint_as_float(v[j + 1]) * __shfl_sync(0xffffffffu, rw, j + 1);
-              const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-              const __nv_bfloat162 o = odd ? __floats2bfloat162_rn(other, v1) : __floats2bfloat162_rn(v0, other);
-              if (live && j + odd < left) *reinterpret_cast<__nv_bfloat162 *>(y + (long)j * p.N) = o;
-            }
-          }
-        }
+        store_tokens(store, tbase, tl.row0, tl.count, tl.m0 + (int)rank * BM, q, 1.0f,
+                     reinterpret_cast<uint8_t *>(staging), sm.wbuf + q * 32);
       } else {
-        // rows of dW: 32 words of each lane's row at a time through this
+        // rows of dW, a lane each: 32 words of every row at a time through this
         // warp's 4 KB (16-byte piece j of row r at j ^ (r % 8)), so that every
         // store writes four whole 128-byte row segments
         uint32_t *stg = staging + q * 32 * 32;
         const int n_first = tl.m0 + (int)rank * BM + q * 32;
         const int rr = lane >> 3, ff = lane & 7;
-        // words staged as fp32 sums, or as bf16 pairs already rounded (bf16
-        // out without a previous value to add: the sum is rounded once either way)
-        const bool fp32 = p.out_f32 || p.accumulate;
-        const int per = fp32 ? 32 : 64;  // columns per round
-#pragma unroll 1
-        for (int c = 0; c < tl.count; c += per) {
+        const bool fp32 = p.out_f32 || p.accumulate;  // words: fp32 sums, or bf16 pairs rounded here
+        if (!fp32) {
+          uint32_t lo[32], hi[32];
           if (have) {
-            uint32_t v[32];
-            if (fp32) {
+            ptx::tmem_ld32(tbase, lo);
+            ptx::tmem_ld32(tbase + 32, hi);
+          }
+#pragma unroll 1
+          for (int c = 0; c < tl.count; c += 64) {
+            uint4 val[8];
+            if (have) {
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int i = 8 * (j & 3) + 2 * k;
+                  const __nv_bfloat162 o =
+                      j < 4 ? __floats2bfloat162_rn(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1]))
+                            : __floats2bfloat162_rn(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1]));
+                  w[k] = *reinterpret_cast<const uint32_t *>(&o);
+                }
+                *reinterpret_cast<uint4 *>(stg + lane * 32 + ((j ^ (lane & 7)) << 2)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+              }
+              if (c + 64 < tl.count) {
+                ptx::tmem_ld32(tbase + c + 64, lo);
+                ptx::tmem_ld32(tbase + c + 96, hi);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int r = 4 * k + rr;
+                val[k] = *reinterpret_cast<const uint4 *>(stg + r * 32 + ((ff ^ (r & 7)) << 2));
+              }
+              __syncwarp();
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) val[k] = make_uint4(0, 0, 0, 0);
+            }
+            const int col = tl.c0 + c + ff * 8;
+            __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out + ((long)tl.e * p.N + n_first + rr) * p.K + col;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (n_first + 4 * k + rr < p.N && col < p.K) *reinterpret_cast<uint4 *>(dst + (long)(4 * k) * p.K) = val[k];
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < tl.count; c += 32) {
+            float4 val[8];
+            if (have) {
+              uint32_t v[32];
               ptx::tmem_ld32(tbase + c, v);
               ptx::tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 8; ++j)
                 *reinterpret_cast<uint4 *>(stg + lane * 32 + ((j ^ (lane & 7)) << 2)) =
                     make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int r = 4 * k + rr;
+                val[k] = *reinterpret_cast<const float4 *>(stg + r * 32 + ((ff ^ (r & 7)) << 2));
+              }
+              __syncwarp();
             } else {
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                ptx::tmem_ld32(tbase + c + half * 32, v);
-                ptx::tmem_ld_wait();
+              for (int k = 0; k < 8; ++k) val[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            const int col = tl.c0 + c + ff * 4;
+            const long at = ((long)tl.e * p.N + n_first + rr) * p.K + col;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  uint32_t w[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const __nv_bfloat162 o = __floats2bfloat162_rn(__uint_as_float(v[8 * j + 2 * k]),
-                                                                   __uint_as_float(v[8 * j + 2 * k + 1]));
-                    w[k] = *reinterpret_cast<const uint32_t *>(&o);
-                  }
-                  *reinterpret_cast<uint4 *>(stg + lane * 32 + (((half * 4 + j) ^ (lane & 7)) << 2)) =
-                      make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 8; ++k) {
+              if (n_first + 4 * k + rr >= p.N || col >= p.K || (!have && p.accumulate)) continue;
+              float4 x = val[k];
+              if (p.out_f32) {
+                float4 *dst = reinterpret_cast<float4 *>((float *)p.out + at + (long)(4 * k) * p.K);
+                if (p.accumulate) {
+                  const float4 old = *dst;
+                  x = make_float4(old.x + x.x, old.y + x.y, old.z + x.z, old.w + x.w);
                 }
+                *dst = x;
+              } else {  // added in fp32, rounded once
+                uint2 *dst = reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.out + at + (long)(4 * k) * p.K);
+                const uint2 old = *dst;
+                const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&old.x));
+                const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&old.y));
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x + x.x, a.y + x.y);
+                const __nv_bfloat162 hi = __floats2bfloat162_rn(b.x + x.z, b.y + x.w);
+                *dst = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
               }
             }
-            __syncwarp();
           }
-          const int col = tl.c0 + c + ff * (fp32 ? 4 : 8);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = 4 * k + rr;
-            if (n_first + r >= p.N || col >= p.K || (!have && p.accumulate)) continue;
-            uint4 val = make_uint4(0, 0, 0, 0);
-            if (have) val = *reinterpret_cast<const uint4 *>(stg + r * 32 + ((ff ^ (r & 7)) << 2));
-            const long at = ((long)tl.e * p.N + n_first + r) * p.K + col;
-            if (!p.accumulate) {
-              *reinterpret_cast<uint4 *>((uint8_t *)p.out + at * (p.out_f32 ? 4 : 2)) = val;
-              continue;
-            }
-            const float4 sum = make_float4(__uint_as_float(val.x), __uint_as_float(val.y), __uint_as_float(val.z),
-                                           __uint_as_float(val.w));
-            if (p.out_f32) {
-              float4 *dst = reinterpret_cast<float4 *>((float *)p.out + at);
-              const float4 old = *dst;
-              *dst = make_float4(old.x + sum.x, old.y + sum.y, old.z + sum.z, old.w + sum.w);
-            } else {
-              uint2 *dst = reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.out + at);
-              const uint2 old = *dst;
-              const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&old.x));
-              const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&old.y));
-              const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x + sum.x, a.y + sum.y);
-              const __nv_bfloat162 hi = __floats2bfloat162_rn(b.x + sum.z, b.y + sum.w);
-              *dst = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-            }
-          }
-          __syncwarp();
         }
       }
       if (have) {
@@ -562,7 +565,7 @@ moe_status launch(Params &p, const void *a, const void *b, cudaStream_t s) {
   const long tiles = MODE == TN ? (long)p.E * p.m_blocks * p.n_blocks
                                 : ((long)(p.rows + BT - 1) / BT + used) * p.m_blocks;  // at most
   if (tiles > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
-  const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart + (MODE == TN ? kStaging : 0);
+  const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart + kStaging;
   auto kern = grouped_gemm<MODE, BT>;
   static std::atomic<uint64_t> known[kMaxDevices];
   Launch l;

@@ -73,11 +73,12 @@ struct Smem {
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint64_t drain;
+  __align__(16) float wbuf[4 * 32];  // row factors, 32 an epilogue warp
   uint32_t tmem_base;
   int abort;
   int start[MAX_E + 1];
 };
-constexpr int kSmemPart = 4608;
+constexpr int kSmemPart = 5120;
 static_assert(sizeof(Smem<8>) <= kSmemPart, "barriers and tile list");
 
 struct Params {
@@ -143,6 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *stage_sa = stage_b + STAGES * C::B_BYTES;
   uint8_t *stage_sb = stage_sa + STAGES * C::SA_BYTES;
   Smem<STAGES> &sm = *reinterpret_cast<Smem<STAGES> *>(stage_sb + STAGES * C::SB_BYTES);
+
+  uint8_t *staging = reinterpret_cast<uint8_t *>(&sm) + kSmemPart;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -344,49 +347,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================================================= epilogue (warps 2..5)
     const int q = warp & 3;
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    const RowStore store = {p.out, p.out_f32, p.N, p.ra, p.row_weight};
     int i = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++i) {
       const TokenTile tl = tile_of(t);
       const int acc = i & 1;
       const uint32_t aph = (i >> 1) & 1u;
       const int n = tl.blk * BM + q * 32 + lane;
-      const bool live = n < p.N;
-      const float wn = p.rw && live ? p.rw[(long)tl.e * p.N + n] : 1.0f;
-      if (!warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status)) break;
+      const float wn = p.rw && n < p.N ? p.rw[(long)tl.e * p.N + n] : 1.0f;
+      if (!epi_all(warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status))) break;
       ptx::tc_fence_after();
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
-#pragma unroll 1
-      for (int c = 0; c < tl.count; c += 32) {
-        uint32_t v[32];
-        ptx::tmem_ld32(tbase + c, v);
-        float rs = 1.0f;
-        if (c + lane < tl.count) {
-          const int r = tl.row0 + c + lane;
-          if (p.ra) rs = p.ra[r];
-          if (p.row_weight) rs *= p.row_weight[r];
-        }
-        ptx::tmem_ld_wait();
-        const int left = tl.count - c;
-        if (p.out_f32) {
-          float *y = (float *)p.out + (long)(tl.row0 + c) * p.N + n;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float w = __shfl_sync(0xffffffffu, rs, j);
-            if (live && j < left) y[(long)j * p.N] = __uint_as_float(v[j]) * wn * w;
-          }
-        } else {
-          const int odd = lane & 1;
-          __nv_bfloat16 *y = (__nv_bfloat16 *)p.out + (long)(tl.row0 + c + odd) * p.N + (n - odd);
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float v0 = __uint_as_float(v[j]) * wn * __shfl_sync(0xffffffffu, rs, j);
-            const float v1 = __uint_as_float(v[j + 1]) * wn * __shfl_sync(0xffffffffu, rs, j + 1);
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-            const __nv_bfloat162 o = odd ? __floats2bfloat162_rn(other, v1) : __floats2bfloat162_rn(v0, other);
-            if (live && j + odd < left) *reinterpret_cast<__nv_bfloat162 *>(y + (long)j * p.N) = o;
-          }
-        }
-      }
+      store_tokens(store, tbase, tl.row0, tl.count, tl.blk * BM, q, wn, staging, sm.wbuf + q * 32);
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.tmem_empty[acc]);
@@ -419,7 +391,7 @@ moe_status launch(Params &p, const void *a, const void *w, cudaStream_t s) {
   const long used = p.rows < p.E ? p.rows : p.E;
   const long tiles = ((long)(p.rows + BT - 1) / BT + used) * p.m_blocks;
   if (tiles > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
-  const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart;
+  const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart + kRowStage;
   auto kern = grouped_gemm_fp4<BT, SF_TMA>;
   static std::atomic<uint64_t> known[kMaxDevices];
   Launch l;

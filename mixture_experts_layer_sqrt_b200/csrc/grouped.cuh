@@ -198,5 +198,110 @@ __device__ __forceinline__ TokenTile token_tile(const int *start, const int32_t 
   return r;
 }
 
+// ---------------------------------------------------------------- epilogue
+// Four warps store a tile of 128 output features (TMEM lanes) x `count` tokens
+// (columns) to rows of y [rows, N].
+//
+// bf16: a lane holds one feature of 32 tokens.  Lanes exchange halves so that
+// each holds pairs of features, the four warps put 32 tokens x 128 features
+// into shared memory (256 bytes a token; the 64-byte quarter of warp q of token
+// t at q ^ (t & 1), so that the two tokens of a store take all banks), and each
+// warp writes whole 256-byte rows of 8 tokens.  Two buffers, one barrier a
+// round.  fp32: a warp's store is 128 bytes of a row as it is.
+constexpr int kRowStage = 2 * 32 * 256;  // bytes
+constexpr int kEpiBarrier = 1;           // named barrier of the 128 epilogue threads
+
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync %0, 128;" ::"n"(kEpiBarrier) : "memory"); }
+// The same decision for all epilogue warps: true if `ok` is in every thread.
+__device__ __forceinline__ bool epi_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "n"(kEpiBarrier)
+      : "memory");
+  return r != 0;
+}
+
+struct RowStore {
+  void *out;
+  int out_f32;
+  int N;
+  const float *w0, *w1;  // factors of a row [rows], or null
+};
+
+// q: this warp's lane quadrant; n0: the tile's first feature; scale: this
+// lane's feature factor.  stage: kRowStage bytes shared by the four warps;
+// wbuf: 32 floats of this warp's.
+__device__ __forceinline__ void store_tokens(const RowStore &o, uint32_t tbase, int row0, int count, int n0, int q,
+                                             float scale, uint8_t *stage, float *wbuf) {
+  const int lane = threadIdx.x & 31;
+  const int n = n0 + q * 32 + lane;
+  const bool weighted = o.w0 || o.w1;
+  const int odd = lane & 1;
+  uint32_t v[32];
+  ptx::tmem_ld32(tbase, v);
+#pragma unroll 1
+  for (int c = 0; c < count; c += 32) {
+    const int left = count - c;
+    if (weighted) {
+      float w = 1.0f;
+      if (lane < left) {
+        if (o.w0) w = o.w0[row0 + c + lane];
+        if (o.w1) w *= o.w1[row0 + c + lane];
+      }
+      __syncwarp();
+      wbuf[lane] = w;
+      __syncwarp();
+    }
+    ptx::tmem_ld_wait();
+    float f[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]) * scale;
+    if (weighted) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 w = *reinterpret_cast<const float4 *>(wbuf + j);
+        f[j] *= w.x, f[j + 1] *= w.y, f[j + 2] *= w.z, f[j + 3] *= w.w;
+      }
+    }
+    if (c + 32 < count) ptx::tmem_ld32(tbase + c + 32, v);
+    if (o.out_f32) {
+      float *y = (float *)o.out + (long)(row0 + c) * o.N + n;
+      if (n < o.N) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j < left) y[(long)j * o.N] = f[j];
+      }
+      continue;
+    }
+    uint8_t *buf = stage + ((c >> 5) & 1) * (kRowStage / 2);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      // the even lane keeps token j, features (n, n + 1); the odd one token j + 1, (n - 1, n)
+      const float other = __shfl_xor_sync(0xffffffffu, odd ? f[j] : f[j + 1], 1);
+      const __nv_bfloat162 p = odd ? __floats2bfloat162_rn(other, f[j + 1]) : __floats2bfloat162_rn(f[j], other);
+      *reinterpret_cast<__nv_bfloat162 *>(buf + (j + odd) * 256 + ((q ^ odd) << 6) + ((lane & ~1) << 1)) = p;
+    }
+    epi_sync();
+    // this warp's 8 tokens, two a round: 16 lanes x 16 bytes each
+    const int piece = lane & 15, half = lane >> 4;
+    const bool in = n0 + piece * 8 < o.N;
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = q * 8 + 2 * i + half;
+      w[i] = *reinterpret_cast<const uint4 *>(buf + t * 256 + (((piece >> 2) ^ (t & 1)) << 6) + ((piece & 3) << 4));
+    }
+    __nv_bfloat16 *y = (__nv_bfloat16 *)o.out + (long)(row0 + c + q * 8 + half) * o.N + n0 + piece * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (in && q * 8 + 2 * i + half < left) *reinterpret_cast<uint4 *>(y + (long)(2 * i) * o.N) = w[i];
+  }
+}
+
 }  // namespace grouped
 }  // namespace moe
