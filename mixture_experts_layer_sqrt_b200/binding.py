@@ -491,13 +491,13 @@ def _live(offsets: Optional[torch.Tensor]):
     return offsets.data_ptr() + 4 * (offsets.numel() - 1)
 
 
-def _nvfp4_outputs(rows: int, cols: int, dev, row_scaled: bool, values: bool, out) -> Dict[str, torch.Tensor]:
+def _nvfp4_outputs(rows: int, cols: int, x: torch.Tensor, row_scaled: bool, values: bool, out) -> Dict[str, torch.Tensor]:
     if out is None:
         u8 = torch.uint8
-        return dict(codes=torch.empty((rows, cols // 2), dtype=u8, device=dev),
-                    scales=torch.empty((rows, cols // 16), dtype=u8, device=dev),
-                    row_scale=torch.empty(rows, dtype=torch.float32, device=dev) if row_scaled else None,
-                    values=torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if values else None)
+        return dict(codes=x.new_empty((rows, cols // 2), dtype=u8),
+                    scales=x.new_empty((rows, cols // 16), dtype=u8),
+                    row_scale=x.new_empty((rows,), dtype=torch.float32) if row_scaled else None,
+                    values=x.new_empty((rows, cols), dtype=torch.bfloat16) if values else None)
     if (out.get("row_scale") is not None and not row_scaled) or (out.get("values") is not None and not values):
         raise ValueError("out has a tensor that this call does not write")
     _need(out.get("codes"), (rows, cols // 2), torch.uint8, "codes")
@@ -527,7 +527,7 @@ def quantize_nvfp4(x: torch.Tensor, row_token: Optional[torch.Tensor] = None, of
     if _elsewhere(d, stream):
         with _on(d, stream):
             return quantize_nvfp4(x, row_token, offsets, row_scaled, values, out)
-    o = _nvfp4_outputs(rows, cols, x.device, row_scaled, values, out)
+    o = _nvfp4_outputs(rows, cols, x, row_scaled, values, out)
     _check(lib.moe_quantize_nvfp4(rows, cols, dt, _p(x), x_rows, _p(row_token), _live(offsets), _p(o["codes"]),
                                   _p(o["scales"]), _p(o["row_scale"]), _p(o["values"]), _raw_stream(d)),
            "moe_quantize_nvfp4")
@@ -551,7 +551,7 @@ def swiglu_quantize_nvfp4(gu: torch.Tensor, clamp: float = 0.0, clamp_mode="prea
     if _elsewhere(d, stream):
         with _on(d, stream):
             return swiglu_quantize_nvfp4(gu, clamp, clamp_mode, offsets, row_scaled, values, out)
-    o = _nvfp4_outputs(rows, cols, gu.device, row_scaled, values, out)
+    o = _nvfp4_outputs(rows, cols, gu, row_scaled, values, out)
     _check(lib.moe_swiglu_quantize_nvfp4(rows, cols, dt, _p(gu), clamp, CLAMP_MODES[clamp_mode], _live(offsets),
                                          _p(o["codes"]), _p(o["scales"]), _p(o["row_scale"]), _p(o["values"]),
                                          _raw_stream(d)), "moe_swiglu_quantize_nvfp4")

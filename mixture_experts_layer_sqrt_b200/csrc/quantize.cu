@@ -12,16 +12,19 @@
 // an infinity or a NaN gets the NaN scale (0x7f), takes no part in the row's
 // scale and has codes 0: the failure stays visible.
 //
-// bf16 sources: x / (s rs) is formed as x times the rounded reciprocal and
-// then rounded to 18 significant bits.  x has 8 bits and s 4, so a quotient
-// that is not exactly on one of e2m1's seven ties is at least 1/256 (relative)
-// away from it, and one that is on it is restored by that rounding: the codes
-// are those of the exact quotient.  fp32 sources divide.
+// bf16 sources: x / (s rs) is formed as x times (1 + 2^-20) times the rounded
+// reciprocal, cut to 18 significant bits.  The product is off by at most 2^-22,
+// so a quotient that is exactly one of e2m1's seven ties comes out just above
+// it and is cut back onto it; x has 8 bits and s 4, so any other is at least
+// 1/256 (relative) away and stays on its side: the codes are those of the exact
+// quotient.  blockmax / 6 in the same way (8 bits against e4m3's 5-bit ties).
+// fp32 sources divide.
 //
 // Sources: rows as they lie or through a row map (the dispatch gather done in
 // 4 bits), or SwiGLU of gate|up rows, rounded to the rows' type first.  A warp
-// per row; a row of up to 32 * 16 * G elements stays in registers between the
-// row maximum and the codes, longer rows are read twice (from L2).
+// per 512 * kHeld elements of a row, up to four: they stay in registers between
+// the row maximum and the codes; longer rows are read twice (from L2).  With few
+// rows four warps share one whatever its length.
 #include <cuda_fp8.h>
 
 #include "act.cuh"
@@ -33,19 +36,27 @@ MOE_VIOLATION_COUNTER(violations_quantize)
 
 namespace {
 
-constexpr int kWarps = 4;  // per block
+// Warps per block: four rows of one warp each, or one row of SPAN warps.
+template <int SPAN>
+constexpr int kWarps = SPAN == 1 ? 4 : SPAN;
 
 template <typename T>
 struct Group;  // 16 elements of a row
 template <>
 struct Group<__nv_bfloat16> {
-  static constexpr int kHeld = 8;  // groups a lane holds
   uint32_t w[8];
+  template <bool WIDE>  // 32-byte aligned
   __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    if constexpr (WIDE) {
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "l"(p));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
-      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      for (int i = 0; i < 2; ++i) {
+        const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
     }
   }
   __device__ __forceinline__ float get(int i) const {
@@ -66,8 +77,8 @@ struct Group<__nv_bfloat16> {
 };
 template <>
 struct Group<float> {
-  static constexpr int kHeld = 4;
   float w[16];
+  template <bool WIDE>
   __device__ __forceinline__ void load(const float *p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -99,16 +110,22 @@ __device__ __forceinline__ int row_exponent(float a) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Two codes, `lo` in bits [3:0].
-__device__ __forceinline__ uint32_t e2m1_pair(float hi, float lo) {
+// Eight codes of t[0..7], element 0 in bits [3:0].
+__device__ __forceinline__ uint32_t e2m1x8(const float *t) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-      "cvt.u32.u8 %0, b;\n\t}\n"
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}\n"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(t[0]), "f"(t[1]), "f"(t[2]), "f"(t[3]), "f"(t[4]), "f"(t[5]), "f"(t[6]), "f"(t[7]));
   return r;
 }
+// 18 significant bits.
+__device__ __forceinline__ float cut(float v) { return __uint_as_float(__float_as_uint(v) & ~0x3Fu); }
+constexpr float kBump = 1.0f + 9.5367431640625e-07f;  // 1 + 2^-20
 
 struct Out {
   uint8_t *codes, *scales;
@@ -116,44 +133,35 @@ struct Out {
   __nv_bfloat16 *values;  // or null
 };
 
-// Codes, scale and values of one group; rs = 2^e.
-template <typename T>
-__device__ __forceinline__ void emit(const Group<T> &g, int e, long row, int cols, int group, const Out &o) {
-  const float a = g.amax();
+// Codes, scale and values (where asked for) of one group with largest magnitude a.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void emit(const Group<T> &g, float a, float rs, float inv_rs, uint2 *codes, uint8_t *scales,
+                                     __nv_bfloat16 *values) {
   const bool bad = !finite(a);
-  const float s0 = __fdiv_rn(a * pow2(-e), 6.0f);
+  const float a_rs = a * inv_rs;
+  const float s0 = sizeof(T) == 2 ? cut(a_rs * ((1.0f / 6.0f) * kBump)) : __fdiv_rn(a_rs, 6.0f);
   uint32_t s8 = bad ? 0x7Fu : (uint32_t)__nv_cvt_float_to_fp8(s0, __NV_SATFINITE, __NV_E4M3);
   __nv_fp8_e4m3 sc;
   sc.__x = (__nv_fp8_storage_t)s8;
   const float s = (float)sc;
-  const float d = s * pow2(e);
-  const bool live = s > 0.0f;  // false for the NaN scale too
-  uint32_t q[2] = {0, 0};
-  if constexpr (sizeof(T) == 2) {
-    const float r = live ? __frcp_rn(d) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float t[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float x = live ? g.get(2 * i + k) : 0.0f;
-        t[k] = __uint_as_float((__float_as_uint(x * r) + 0x20u) & ~0x3Fu);
-      }
-      q[i >> 2] |= e2m1_pair(t[1], t[0]) << (8 * (i & 3));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float t[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) t[k] = live ? __fdiv_rn(g.get(2 * i + k), d) : 0.0f;
-      q[i >> 2] |= e2m1_pair(t[1], t[0]) << (8 * (i & 3));
-    }
+  const float d = s * rs;
+  uint32_t q[2];
+  float r = 0.0f;
+  if (sizeof(T) == 2) {
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    r *= kBump;
   }
-  const long at = row * (cols / 16) + group;
-  reinterpret_cast<uint2 *>(o.codes)[at] = make_uint2(q[0], q[1]);
-  o.scales[at] = (uint8_t)s8;
-  if (o.values) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = sizeof(T) == 2 ? cut(g.get(8 * i + k) * r) : __fdiv_rn(g.get(8 * i + k), d);
+    q[i] = e2m1x8(t);
+  }
+  if (!(s > 0.0f)) q[0] = q[1] = 0;  // zero or NaN scale
+  *codes = make_uint2(q[0], q[1]);
+  *scales = (uint8_t)s8;
+  if (values) {
     uint32_t v[8];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -173,24 +181,44 @@ __device__ __forceinline__ void emit(const Group<T> &g, int e, long row, int col
         v[4 * w + j] = *reinterpret_cast<const uint32_t *>(&b);
       }
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(o.values + (row * cols + group * 16));
-    dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    if (WIDE) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(values), "r"(v[0]), "r"(v[1]),
+                   "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                   : "memory");
+    } else {
+      reinterpret_cast<uint4 *>(values)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<uint4 *>(values)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
   }
 }
 
-template <typename T, bool SWIGLU>
-__global__ void __launch_bounds__(32 * kWarps)
-    quantize_kernel(int rows, int cols, const T *src, int src_rows, const int32_t *row_token, const int32_t *live,
-                    float limit, int mode, Out o) {
-  constexpr int G = Group<T>::kHeld;
+constexpr int kRows = 3;  // a source of rows; 0..2: gate|up with that clamp
+
+// Groups that a lane holds.  bf16, 8192 x 4096 gathered six times / 16384 x 4096
+// from gate|up: 8 groups 123 / 135 us, 4 groups 133 / 107, 2 groups 130 / 94:
+// copying rows wants the fewest instructions, the exponentials more warps.
+template <typename T, int SRC>
+constexpr int kHeld = (SRC == kRows ? 8 : 2) * 2 / (int)sizeof(T);
+
+// WIDE: rows and values
+// are 32-byte aligned, moved 32 bytes a lane.
+template <typename T, int SRC, bool WIDE, int SPAN>
+__global__ void __launch_bounds__(32 * kWarps<SPAN>)
+    quantize_kernel(int rows, int cols, const T *__restrict__ src, int src_rows, const int32_t *__restrict__ row_token,
+                    const int32_t *live, float limit, Out o) {
+  constexpr int G = kHeld<T, SRC>;
+  constexpr bool SWIGLU = SRC != kRows;
   int n_rows = rows;
   if (live) n_rows = *live < 0 ? 0 : (*live < rows ? *live : rows);
-  const int lane = threadIdx.x & 31;
+  // SPAN warps a row: warp `part` of them holds every SPAN-th run of 32 groups
+  __shared__ float part_max[2][SPAN];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = warp % SPAN;
   const int groups = cols / 16;
-  const int chunks = (groups + 32 * G - 1) / (32 * G);
-  const long stride = (long)gridDim.x * kWarps;
-  for (long r = (long)blockIdx.x * kWarps + (threadIdx.x >> 5); r < n_rows; r += stride) {
+  const int chunks = (groups + 32 * SPAN * G - 1) / (32 * SPAN * G);
+  constexpr int RPB = kWarps<SPAN> / SPAN;  // rows a block
+  int turn = 0;
+  for (long r = (long)blockIdx.x * RPB + warp / SPAN; r < n_rows; r += (long)gridDim.x * RPB) {
     long at = r;
     if (!SWIGLU && row_token) {
       at = row_token[r];
@@ -201,20 +229,27 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
     const T *x = src + at * (SWIGLU ? 2l : 1l) * cols;
     Group<T> g[G];
+    float a[G];
     auto load = [&](int chunk) {
 #pragma unroll
       for (int i = 0; i < G; ++i) {
-        const int c = (chunk * G + i) * 32 + lane;
+        const int c = ((chunk * G + i) * SPAN + part) * 32 + lane;
+        if (c < groups) g[i].template load<WIDE>(x + c * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int c = ((chunk * G + i) * SPAN + part) * 32 + lane;
+        a[i] = 0.0f;
         if (c >= groups) continue;
-        g[i].load(x + c * 16);
         if (SWIGLU) {
           Group<T> u;
-          u.load(x + cols + c * 16);
+          u.template load<WIDE>(x + cols + c * 16);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            g[i].set_pair(k, swiglu_of(g[i].get(2 * k), u.get(2 * k), limit, mode),
-                          swiglu_of(g[i].get(2 * k + 1), u.get(2 * k + 1), limit, mode));
+            g[i].set_pair(k, swiglu_of<SRC>(g[i].get(2 * k), u.get(2 * k), limit),
+                          swiglu_of<SRC>(g[i].get(2 * k + 1), u.get(2 * k + 1), limit));
         }
+        a[i] = g[i].amax();
       }
     };
     int e = 0;
@@ -223,35 +258,79 @@ __global__ void __launch_bounds__(32 * kWarps)
       for (int ch = 0; ch < chunks; ++ch) {
         load(ch);
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-          if ((ch * G + i) * 32 + lane >= groups) continue;
-          const float a = g[i].amax();
-          if (finite(a)) m = fmaxf(m, a);
-        }
+        for (int i = 0; i < G; ++i)
+          if (finite(a[i])) m = fmaxf(m, a[i]);
       }
 #pragma unroll
       for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      if (SPAN > 1) {  // the row's warps agree (two sets of slots: one barrier a row is enough)
+        if (lane == 0) part_max[turn][part] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < SPAN; ++i) m = fmaxf(m, part_max[turn][i]);
+        turn ^= 1;
+      }
       e = row_exponent(m);
-      if (lane == 0) o.row_scale[r] = pow2(e);
+      if (lane == 0 && part == 0) o.row_scale[r] = pow2(e);
     }
+    const float rs = pow2(e), inv_rs = pow2(-e);
     for (int ch = 0; ch < chunks; ++ch) {
       if (chunks > 1 || !o.row_scale) load(ch);
+      const int c0 = (ch * G * SPAN + part) * 32 + lane;
+      uint2 *codes = reinterpret_cast<uint2 *>(o.codes) + r * groups + c0;
+      uint8_t *scales = o.scales + r * groups + c0;
+      __nv_bfloat16 *values = o.values ? o.values + (r * cols + c0 * 16) : nullptr;
 #pragma unroll
       for (int i = 0; i < G; ++i) {
-        const int c = (ch * G + i) * 32 + lane;
-        if (c < groups) emit(g[i], e, r, cols, c, o);
+        constexpr int step = 32 * SPAN;
+        if (c0 + i * step < groups)
+          emit<T, WIDE>(g[i], a[i], rs, inv_rs, codes + i * step, scales + i * step,
+                        values ? values + i * step * 16 : nullptr);
       }
     }
   }
 }
 
-template <typename T, bool SWIGLU>
+template <typename T, int SRC, bool WIDE, int SPAN>
+void launch_rows(int rows, int cols, const void *src, int src_rows, const int32_t *row_token, const int32_t *live,
+                 float limit, const Out &o, int sms, cudaStream_t s) {
+  constexpr int RPB = kWarps<SPAN> / SPAN;
+  const long want = ((long)rows + RPB - 1) / RPB, most = (long)sms * 32;
+  quantize_kernel<T, SRC, WIDE, SPAN><<<(int)(want < most ? want : most), 32 * kWarps<SPAN>, 0, s>>>(
+      rows, cols, (const T *)src, src_rows, row_token, live, limit, o);
+}
+
+template <typename T, int SRC, bool WIDE>
+void launch_span(int rows, int cols, const void *src, int src_rows, const int32_t *row_token, const int32_t *live,
+                 float limit, const Out &o, int sms, cudaStream_t s) {
+  constexpr int held = 32 * 16 * kHeld<T, SRC>;  // elements a warp
+  if (rows < sms * 4 || cols > 2 * held)
+    launch_rows<T, SRC, WIDE, 4>(rows, cols, src, src_rows, row_token, live, limit, o, sms, s);
+  else if (cols > held)
+    launch_rows<T, SRC, WIDE, 2>(rows, cols, src, src_rows, row_token, live, limit, o, sms, s);
+  else
+    launch_rows<T, SRC, WIDE, 1>(rows, cols, src, src_rows, row_token, live, limit, o, sms, s);
+}
+
+template <typename T, int SRC>
 void launch_one(int rows, int cols, const void *src, int src_rows, const int32_t *row_token, const int32_t *live,
-                float limit, int mode, const Out &o, int sms, cudaStream_t s) {
-  const long want = ((long)rows + kWarps - 1) / kWarps;
-  const int grid = (int)(want < (long)sms * 16 ? want : (long)sms * 16);
-  quantize_kernel<T, SWIGLU><<<grid, 32 * kWarps, 0, s>>>(rows, cols, (const T *)src, src_rows, row_token, live, limit,
-                                                          mode, o);
+                float limit, const Out &o, int sms, cudaStream_t s) {
+  // rows are a multiple of 32 bytes; the base addresses may be 16-byte aligned only
+  const bool wide = (((uintptr_t)src | (uintptr_t)o.values) & 31u) == 0;
+  if (wide) launch_span<T, SRC, true>(rows, cols, src, src_rows, row_token, live, limit, o, sms, s);
+  else launch_span<T, SRC, false>(rows, cols, src, src_rows, row_token, live, limit, o, sms, s);
+}
+
+template <typename T>
+void launch_type(int rows, int cols, bool swiglu, const void *src, int src_rows, const int32_t *row_token,
+                 const int32_t *live, float limit, int mode, const Out &o, int sms, cudaStream_t s) {
+  const int kind = swiglu ? clamp_kind(limit, mode) : kRows;
+  switch (kind) {
+    case kNoClamp: launch_one<T, kNoClamp>(rows, cols, src, src_rows, row_token, live, limit, o, sms, s); break;
+    case kClampPre: launch_one<T, kClampPre>(rows, cols, src, src_rows, row_token, live, limit, o, sms, s); break;
+    case kClampOut: launch_one<T, kClampOut>(rows, cols, src, src_rows, row_token, live, limit, o, sms, s); break;
+    default: launch_one<T, kRows>(rows, cols, src, src_rows, row_token, live, limit, o, sms, s); break;
+  }
 }
 
 }  // namespace
@@ -263,13 +342,10 @@ moe_status launch_quantize_nvfp4(int rows, int cols, moe_dtype dtype, bool swigl
   MOE_CUDA_TRY(cudaGetDevice(&dev));
   MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   const Out o = {(uint8_t *)codes, (uint8_t *)scales, row_scale, (__nv_bfloat16 *)values};
-  if (dtype == MOE_F32) {
-    if (swiglu) launch_one<float, true>(rows, cols, src, src_rows, row_token, live, limit, mode, o, sms, s);
-    else launch_one<float, false>(rows, cols, src, src_rows, row_token, live, limit, mode, o, sms, s);
-  } else {
-    if (swiglu) launch_one<__nv_bfloat16, true>(rows, cols, src, src_rows, row_token, live, limit, mode, o, sms, s);
-    else launch_one<__nv_bfloat16, false>(rows, cols, src, src_rows, row_token, live, limit, mode, o, sms, s);
-  }
+  if (dtype == MOE_F32)
+    launch_type<float>(rows, cols, swiglu, src, src_rows, row_token, live, limit, mode, o, sms, s);
+  else
+    launch_type<__nv_bfloat16>(rows, cols, swiglu, src, src_rows, row_token, live, limit, mode, o, sms, s);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }

@@ -22,6 +22,28 @@ namespace {
 
 constexpr int kWarps = 8;  // per block
 
+// 16 bytes of T from fp32 values, each rounded once.
+template <typename T>
+__device__ __forceinline__ Vec16<T> pack16(const float *f);
+template <>
+__device__ __forceinline__ Vec16<float> pack16<float>(const float *f) {
+  Vec16<float> r;
+  r.v = make_float4(f[0], f[1], f[2], f[3]);
+  return r;
+}
+template <>
+__device__ __forceinline__ Vec16<__nv_bfloat16> pack16<__nv_bfloat16>(const float *f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&p);
+  }
+  Vec16<__nv_bfloat16> r;
+  r.v = make_uint4(w[0], w[1], w[2], w[3]);
+  return r;
+}
+
 __device__ __forceinline__ int live_rows_of(int rows, const int32_t *live) {
   if (!live) return rows;
   const int n = *live;
@@ -29,9 +51,9 @@ __device__ __forceinline__ int live_rows_of(int rows, const int32_t *live) {
 }
 
 // SPAN: warps a row (1 or kWarps)
-template <typename T, int SPAN>
-__global__ void __launch_bounds__(32 * kWarps) swiglu_kernel(int rows, int F, const T *gu, float limit, int mode,
-                                                             const int32_t *live, T *h) {
+template <typename T, int SPAN, int CLAMP>
+__global__ void __launch_bounds__(32 * kWarps) swiglu_kernel(int rows, int F, const T *__restrict__ gu, float limit,
+                                                             const int32_t *live, T *__restrict__ h) {
   constexpr int V = Vec16<T>::N;
   const int n_rows = live_rows_of(rows, live);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -39,21 +61,26 @@ __global__ void __launch_bounds__(32 * kWarps) swiglu_kernel(int rows, int F, co
   const int part = warp % SPAN;
   for (long r = (long)blockIdx.x * RPB + warp / SPAN; r < n_rows; r += (long)gridDim.x * RPB) {
     const T *g = gu + r * 2 * F, *u = g + F;
+    constexpr int step = SPAN * 32 * V;
+    int c = (part * 32 + lane) * V;
+    Vec16<T> gn, un;  // the next piece, loaded ahead
+    if (c < F) gn = load16(g + c), un = load16(u + c);
 #pragma unroll 2
-    for (int c = (part * 32 + lane) * V; c < F; c += SPAN * 32 * V) {
-      const Vec16<T> gv = load16(g + c), uv = load16(u + c);
-      Vec16<T> o;
+    for (; c < F; c += step) {
+      const Vec16<T> gv = gn, uv = un;
+      if (c + step < F) gn = load16(g + c + step), un = load16(u + c + step);
+      float o[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) o.set(j, swiglu_of(gv.get(j), uv.get(j), limit, mode));
-      store16(h + r * F + c, o);
+      for (int j = 0; j < V; ++j) o[j] = swiglu_of<CLAMP>(gv.get(j), uv.get(j), limit);
+      store16(h + r * F + c, pack16<T>(o));
     }
   }
 }
 
-template <typename T, int SPAN>
+template <typename T, int SPAN, int CLAMP>
 __global__ void __launch_bounds__(32 * kWarps)
-    swiglu_backward_kernel(int rows, int F, const T *gu, const T *dh, const float *row_weight, float limit, int mode,
-                           const int32_t *live, T *dgu, T *hw, float *drow_weight) {
+    swiglu_backward_kernel(int rows, int F, const T *gu, const T *__restrict__ dh, const float *__restrict__ row_weight,
+                           float limit, const int32_t *live, T *dgu, T *__restrict__ hw, float *drow_weight) {
   constexpr int V = Vec16<T>::N;
   __shared__ float part_sum[kWarps];
   const int n_rows = live_rows_of(rows, live);
@@ -65,35 +92,40 @@ __global__ void __launch_bounds__(32 * kWarps)
     T *dgp = dgu + r * 2 * F, *dup = dgp + F;
     const float w = row_weight ? row_weight[r] : 1.0f;
     float sum = 0.0f;
-#pragma unroll 2
-    for (int c = (part * 32 + lane) * V; c < F; c += SPAN * 32 * V) {
-      const Vec16<T> gv = load16(gp + c), uv = load16(up + c), dv = load16(dp + c);
-      Vec16<T> og, ou, oh;
+    constexpr int step = SPAN * 32 * V;
+    int c = (part * 32 + lane) * V;
+    Vec16<T> gn, un, dn;  // the next piece, loaded ahead
+    if (c < F) gn = load16(gp + c), un = load16(up + c), dn = load16(dp + c);
+#pragma unroll 1
+    for (; c < F; c += step) {
+      const Vec16<T> gv = gn, uv = un, dv = dn;
+      if (c + step < F) gn = load16(gp + c + step), un = load16(up + c + step), dn = load16(dp + c + step);
+      float og[V], ou[V], oh[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float g0 = gv.get(j), u0 = uv.get(j), d = dv.get(j);
-        const bool pre = limit > 0.0f && mode == MOE_CLAMP_PREACT;
-        const float g = pre ? clip(g0, limit) : g0, u = pre ? clip(u0, limit) : u0;
-        const float s = sigmoid_f32(g);
-        const float silu = g * s;
+        const float g = CLAMP == kClampPre ? clip(g0, limit) : g0, u = CLAMP == kClampPre ? clip(u0, limit) : u0;
+        const float s = sizeof(T) == 2 ? sigmoid_fast(g) : sigmoid_f32(g);
+        const float silu = g * s, dw = d * w;
         float h = silu * u;
-        float dg = d * w * u * (s * (1.0f + g * (1.0f - s))), du = d * w * silu;
-        if (pre) {
-          if (fabsf(g0) > limit) dg = 0.0f;
-          if (fabsf(u0) > limit) du = 0.0f;
-        } else if (limit > 0.0f && fabsf(h) > limit) {
+        og[j] = dw * u * fmaf(silu, 1.0f - s, s);
+        ou[j] = dw * silu;
+        if (CLAMP == kClampPre) {
+          if (fabsf(g0) > limit) og[j] = 0.0f;
+          if (fabsf(u0) > limit) ou[j] = 0.0f;
+        } else if (CLAMP == kClampOut) {
+          if (fabsf(h) > limit) {
+            og[j] = 0.0f;
+            ou[j] = 0.0f;
+          }
           h = clip(h, limit);
-          dg = 0.0f;
-          du = 0.0f;
         }
-        og.set(j, dg);
-        ou.set(j, du);
-        oh.set(j, w * h);
-        sum += d * h;
+        oh[j] = w * h;
+        sum = fmaf(d, h, sum);
       }
-      store16(dgp + c, og);
-      store16(dup + c, ou);
-      if (hw) store16(hw + r * F + c, oh);
+      store16(dgp + c, pack16<T>(og));
+      store16(dup + c, pack16<T>(ou));
+      if (hw) store16(hw + r * F + c, pack16<T>(oh));
     }
     if (drow_weight) {
 #pragma unroll
@@ -129,27 +161,36 @@ inline int grid_for(int rows, int sms, bool spread_rows) {
   return (int)(blocks < (long)sms * 8 ? blocks : (long)sms * 8);
 }
 
-template <typename T>
-void forward(int rows, int F, const void *gu, float limit, int mode, const int32_t *live, void *h, int sms,
-             cudaStream_t s) {
+template <typename T, int CLAMP>
+void forward(int rows, int F, const void *gu, float limit, const int32_t *live, void *h, int sms, cudaStream_t s) {
   const bool sp = spread(rows, sms);
   const int grid = grid_for(rows, sms, sp);
-  if (sp) swiglu_kernel<T, kWarps><<<grid, 32 * kWarps, 0, s>>>(rows, F, (const T *)gu, limit, mode, live, (T *)h);
-  else swiglu_kernel<T, 1><<<grid, 32 * kWarps, 0, s>>>(rows, F, (const T *)gu, limit, mode, live, (T *)h);
+  if (sp) swiglu_kernel<T, kWarps, CLAMP><<<grid, 32 * kWarps, 0, s>>>(rows, F, (const T *)gu, limit, live, (T *)h);
+  else swiglu_kernel<T, 1, CLAMP><<<grid, 32 * kWarps, 0, s>>>(rows, F, (const T *)gu, limit, live, (T *)h);
 }
 
-template <typename T>
-void backward(int rows, int F, const void *gu, const void *dh, const float *rw, float limit, int mode,
-              const int32_t *live, void *dgu, void *hw, float *drw, int sms, cudaStream_t s) {
+template <typename T, int CLAMP>
+void backward(int rows, int F, const void *gu, const void *dh, const float *rw, float limit, const int32_t *live,
+              void *dgu, void *hw, float *drw, int sms, cudaStream_t s) {
   const bool sp = spread(rows, sms);
   const int grid = grid_for(rows, sms, sp);
   if (sp)
-    swiglu_backward_kernel<T, kWarps><<<grid, 32 * kWarps, 0, s>>>(rows, F, (const T *)gu, (const T *)dh, rw, limit,
-                                                                   mode, live, (T *)dgu, (T *)hw, drw);
+    swiglu_backward_kernel<T, kWarps, CLAMP><<<grid, 32 * kWarps, 0, s>>>(rows, F, (const T *)gu, (const T *)dh, rw,
+                                                                          limit, live, (T *)dgu, (T *)hw, drw);
   else
-    swiglu_backward_kernel<T, 1><<<grid, 32 * kWarps, 0, s>>>(rows, F, (const T *)gu, (const T *)dh, rw, limit, mode,
-                                                              live, (T *)dgu, (T *)hw, drw);
+    swiglu_backward_kernel<T, 1, CLAMP><<<grid, 32 * kWarps, 0, s>>>(rows, F, (const T *)gu, (const T *)dh, rw, limit,
+                                                                     live, (T *)dgu, (T *)hw, drw);
 }
+
+// f<T, CLAMP>(args...) for the element type and clamp of the call
+#define MOE_BY_CLAMP(f, T, ...)                                          \
+  do {                                                                   \
+    switch (clamp_kind(limit, mode)) {                                   \
+      case kNoClamp: f<T, kNoClamp>(__VA_ARGS__); break;                 \
+      case kClampPre: f<T, kClampPre>(__VA_ARGS__); break;               \
+      default: f<T, kClampOut>(__VA_ARGS__); break;                      \
+    }                                                                    \
+  } while (0)
 
 }  // namespace
 
@@ -158,8 +199,8 @@ moe_status launch_swiglu(int rows, int F, moe_dtype dtype, const void *gu, float
   int sms = 0;
   moe_status st = device_sms(sms);
   if (st != MOE_OK) return st;
-  if (dtype == MOE_F32) forward<float>(rows, F, gu, limit, mode, live, h, sms, s);
-  else forward<__nv_bfloat16>(rows, F, gu, limit, mode, live, h, sms, s);
+  if (dtype == MOE_F32) MOE_BY_CLAMP(forward, float, rows, F, gu, limit, live, h, sms, s);
+  else MOE_BY_CLAMP(forward, __nv_bfloat16, rows, F, gu, limit, live, h, sms, s);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -171,9 +212,9 @@ moe_status launch_swiglu_backward(int rows, int F, moe_dtype dtype, const void *
   moe_status st = device_sms(sms);
   if (st != MOE_OK) return st;
   if (dtype == MOE_F32)
-    backward<float>(rows, F, gu, dh, row_weight, limit, mode, live, dgu, hw, drow_weight, sms, s);
+    MOE_BY_CLAMP(backward, float, rows, F, gu, dh, row_weight, limit, live, dgu, hw, drow_weight, sms, s);
   else
-    backward<__nv_bfloat16>(rows, F, gu, dh, row_weight, limit, mode, live, dgu, hw, drow_weight, sms, s);
+    MOE_BY_CLAMP(backward, __nv_bfloat16, rows, F, gu, dh, row_weight, limit, live, dgu, hw, drow_weight, sms, s);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
