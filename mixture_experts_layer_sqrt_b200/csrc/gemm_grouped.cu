@@ -98,7 +98,9 @@ static_assert(sizeof(Smem<8>) <= kSmemPart, "the epilogue staging follows the ba
 struct Params {
   int rows, N, K, E;
   int m_blocks;    // TILE_M-feature blocks of the output
-  int n_blocks;    // TN: BT-column blocks
+  int tile;        // tokens or columns of a tile, at most BT
+  int n_blocks;    // TN: blocks of `tile` columns
+  int split;       // parts that a tile's reduction is cut into, one a CTA (or pair) of a cluster
   const int32_t *offsets;
   const float *row_weight;
   void *out;       // y [rows, N] or dW [E, N, K]
@@ -141,10 +143,17 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
 
   constexpr bool PAIR = C::PAIR;
 
+  // split: this CTA's partial sums, over the stage buffers once the MMAs have read them
+  float *parts = reinterpret_cast<float *>(base);
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
-  const int unit = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-  const int n_units = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+  // a cluster: `split` CTAs or pairs, which share a tile
+  const uint32_t crank = ptx::cluster_ctarank();
+  const uint32_t rank = PAIR ? crank & 1u : 0u;     // in the pair
+  const uint32_t lead = crank - rank;               // the pair's leader
+  const int part = PAIR ? (int)(crank >> 1) : (int)crank;
+  const int csize = PAIR ? 2 * p.split : p.split;
+  const int unit = (int)blockIdx.x / csize, n_units = (int)gridDim.x / csize;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -178,7 +187,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   if (warp == 2) {
     // TN needs no tile list (every group has m_blocks * n_blocks tiles), but
     // the same check of the offsets
-    const bool ok = scan_tiles(p.offsets, p.rows, p.E, BT, sm.start);
+    const bool ok = scan_tiles(p.offsets, p.rows, p.E, p.tile, sm.start);
     if (kChecked && !ok && lane == 0 && blockIdx.x == 0) note_violation();
     if (kChecked && MODE == TN && lane == 0) sm.start[0] = ok ? 0 : 1;
   }
@@ -194,7 +203,10 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
 
   // tile t -> group, feature block, first row / column, reduction blocks
   struct Tile {
-    int e, m0, c0, count, row0, red;  // c0: first column (TN); count: tokens or columns; red: reduction length
+    int e, m0, c0, count, row0;  // c0: first column (TN); count: tokens or columns; row0: first token
+    int k0, red;                 // this part's first reduction element (TN: row) and their number
+    int blocks;                  // reduction blocks of all parts
+    __device__ int first_block(int part, int split) const { return (int)((long)blocks * part / split); }
     // MMA N, and the tokens or columns that this CTA stages of it
     __device__ int width() const { return (count + C::N_STEP - 1) & ~(C::N_STEP - 1); }
     __device__ int staged() const { return PAIR ? width() / 2 : width(); }
@@ -207,10 +219,11 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       const int local = t - r.e * per;
       const int nb = local / p.m_blocks;
       r.m0 = (local - nb * p.m_blocks) * C::TILE_M;
-      r.c0 = nb * BT;
-      r.count = p.K - r.c0 < BT ? p.K - r.c0 : BT;
-      r.row0 = seg_begin(p.offsets, p.rows, r.e);
-      r.red = seg_end(p.offsets, p.rows, r.e) - r.row0;
+      r.c0 = nb * p.tile;
+      r.count = p.K - r.c0 < p.tile ? p.K - r.c0 : p.tile;
+      r.row0 = 0;
+      r.k0 = seg_begin(p.offsets, p.rows, r.e);
+      r.red = seg_end(p.offsets, p.rows, r.e) - r.k0;
       if (r.red < 0) r.red = 0;
     } else {
       const TokenTile tt = token_tile(sm.start, p.offsets, p.rows, p.E, p.m_blocks, t, C::N_STEP);
@@ -219,7 +232,15 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       r.c0 = 0;
       r.row0 = tt.row0;
       r.count = tt.count;
+      r.k0 = 0;
       r.red = p.K;
+    }
+    r.blocks = (r.red + BK - 1) / BK;
+    if (p.split > 1) {
+      const int b0 = r.first_block(part, p.split), b1 = r.first_block(part + 1, p.split);
+      r.k0 += b0 * BK;
+      r.red = (b1 * BK < r.red ? b1 * BK : r.red) - b0 * BK;
+      if (r.red < 0) r.red = 0;
     }
     return r;
   };
@@ -247,24 +268,24 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
           uint64_t *bar = &sm.full[ring.s];
           uint8_t *a = stage_a + ring.s * A_BYTES;
           uint8_t *b = stage_b + ring.s * C::B_BYTES;
-          const int k0 = kb * BK;
-          const bool partial = MODE == TN && tl.red - k0 < BK;
+          const int k0 = tl.k0 + kb * BK;
+          const bool partial = MODE == TN && tl.red - kb * BK < BK;
           if (PAIR && !partial) {
             // both CTAs' copies complete on the leader's barrier
-            const uint32_t lead = ptx::map_to_rank(bar, 0);
+            const uint32_t lead_bar = ptx::map_to_rank(bar, lead);
             if (rank == 0) ptx::mbar_arrive_expect_tx(bar, 2 * tx);
             if (MODE == NT) {
-              ptx::tma_load_3d_pair(a, &tmA, lead, k0, m0, tl.e);
+              ptx::tma_load_3d_pair(a, &tmA, lead_bar, k0, m0, tl.e);
             } else if (MODE == NN) {
-              ptx::tma_load_3d_pair(a, &tmA, lead, m0, k0, tl.e);
-              ptx::tma_load_3d_pair(a + BOX, &tmA, lead, m0 + 64, k0, tl.e);
+              ptx::tma_load_3d_pair(a, &tmA, lead_bar, m0, k0, tl.e);
+              ptx::tma_load_3d_pair(a + BOX, &tmA, lead_bar, m0 + 64, k0, tl.e);
             } else {
-              ptx::tma_load_2d_pair(a, &tmA, lead, m0, tl.row0 + k0);
-              ptx::tma_load_2d_pair(a + BOX, &tmA, lead, m0 + 64, tl.row0 + k0);
+              ptx::tma_load_2d_pair(a, &tmA, lead_bar, m0, k0);
+              ptx::tma_load_2d_pair(a + BOX, &tmA, lead_bar, m0 + 64, k0);
             }
             for (int i = 0; i < boxes; ++i) {
-              if (MODE == TN) ptx::tma_load_2d_pair(b + i * BOX, &tmB, lead, b0 + i * 64, tl.row0 + k0);
-              else ptx::tma_load_2d_pair(b + i * C::TOK_BOX * BK * 2, &tmB, lead, k0, b0 + i * C::TOK_BOX);
+              if (MODE == TN) ptx::tma_load_2d_pair(b + i * BOX, &tmB, lead_bar, b0 + i * 64, k0);
+              else ptx::tma_load_2d_pair(b + i * C::TOK_BOX * BK * 2, &tmB, lead_bar, k0, b0 + i * C::TOK_BOX);
             }
             continue;
           }
@@ -280,11 +301,11 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
             ptx::tma_load_3d(a, &tmA, bar, m0, k0, tl.e);
             ptx::tma_load_3d(a + BOX, &tmA, bar, m0 + 64, k0, tl.e);
           } else {
-            ptx::tma_load_2d(a, &tmA, bar, m0, tl.row0 + k0);
-            ptx::tma_load_2d(a + BOX, &tmA, bar, m0 + 64, tl.row0 + k0);
+            ptx::tma_load_2d(a, &tmA, bar, m0, k0);
+            ptx::tma_load_2d(a + BOX, &tmA, bar, m0 + 64, k0);
           }
           for (int i = 0; i < boxes; ++i) {
-            if (MODE == TN) ptx::tma_load_2d(b + i * BOX, &tmB, bar, b0 + i * 64, tl.row0 + k0);
+            if (MODE == TN) ptx::tma_load_2d(b + i * BOX, &tmB, bar, b0 + i * 64, k0);
             else ptx::tma_load_2d(b + i * C::TOK_BOX * BK * 2, &tmB, bar, k0, b0 + i * C::TOK_BOX);
           }
         }
@@ -317,8 +338,9 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
         if (PAIR) ptx::mma_bf16_pair(d, a, b, id, acc);
         else ptx::mma_bf16(d, a, b, id, acc);
       };
-      auto commit = [](uint64_t *bar) {  // pairs: on both CTAs' barriers
-        if (PAIR) ptx::mma_commit_pair_mc(bar, 0x3);
+      const uint16_t both = (uint16_t)(0x3u << lead);
+      auto commit = [both](uint64_t *bar) {  // pairs: on both CTAs' barriers
+        if (PAIR) ptx::mma_commit_pair_mc(bar, both);
         else ptx::mma_commit(bar);
       };
       Ring<STAGES> ring;
@@ -390,7 +412,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (rank != 0) {
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(&sm.cleared[s], 0));
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(&sm.cleared[s], lead));
       } else {
         if (!warp_wait(&sm.cleared[s], phase >> s & 1, &sm.abort, p.status)) break;
         if (lane == 0) ptx::mbar_arrive(&sm.full[s]);
@@ -405,7 +427,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     int i = 0;
     for (int t = unit; t < total; t += n_units) {
       const Tile tl = tile_of(t);
-      const bool have = MODE != TN || tl.red > 0;
+      const bool have = tl.red > 0;
       const int acc = i & 1;
       const uint32_t aph = (i >> 1) & 1u;
       if (have) {
@@ -414,7 +436,9 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
         ptx::tc_fence_after();
       }
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
-      if (MODE != TN) {
+      if (p.split > 1) {
+        if (have) put_part(parts, tbase, tl.count, q);
+      } else if (MODE != TN) {
         store_tokens(store, tbase, tl.row0, tl.count, tl.m0 + (int)rank * BM, q, 1.0f,
                      reinterpret_cast<uint8_t *>(staging), sm.wbuf + q * 32);
       } else {
@@ -524,16 +548,40 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (PAIR) ptx::mbar_arrive_cluster(ptx::map_to_rank(&sm.tmem_empty[acc], 0));
+          if (PAIR) ptx::mbar_arrive_cluster(ptx::map_to_rank(&sm.tmem_empty[acc], lead));
           else ptx::mbar_arrive(&sm.tmem_empty[acc]);
         }
       }
     }
   }
 
+  if (p.split > 1) {
+    // the parts' sums, in the parts' order, each part a share of the columns
+    __syncwarp();
+    ptx::cluster_sync();
+    if (unit < total) {
+      const Tile tl = tile_of(unit);
+      const int c_lo = tl.count * part / p.split, w = tl.count * (part + 1) / p.split - c_lo;
+      const int n0 = tl.m0 + (int)rank * BM;
+      for (int i = threadIdx.x; i < w * BM; i += kThreads<MODE>) {
+        const int f = MODE == TN ? i / w : i % BM, c = c_lo + (MODE == TN ? i - f * w : i / BM);
+        if (n0 + f >= p.N) continue;
+        float sum = 0.0f;
+        for (int k = 0; k < p.split; ++k)
+          if (tl.first_block(k, p.split) < tl.first_block(k + 1, p.split))
+            sum += ld_part(parts + c * kPartPitch + f, PAIR ? 2 * k + rank : (uint32_t)k);
+        if (MODE != TN) {
+          if (p.row_weight) sum *= p.row_weight[tl.row0 + c];
+          put_out(p.out, p.out_f32, (long)(tl.row0 + c) * p.N + n0 + f, sum, false);
+        } else if (tl.blocks > 0 || !p.accumulate) {
+          put_out(p.out, p.out_f32, ((long)tl.e * p.N + n0 + f) * p.K + tl.c0 + c, sum, p.accumulate != 0);
+        }
+      }
+    }
+  }
   ptx::tc_fence_before();
   __syncwarp();
-  if (PAIR) ptx::cluster_sync();  // neither CTA leaves while the pair's copies, MMAs or arrivals are pending
+  if (csize > 1) ptx::cluster_sync();  // neither CTA leaves while the pair's copies, MMAs or arrivals are pending
   else __syncthreads();
   if (warp == 1) {
     __syncwarp();
@@ -559,35 +607,50 @@ moe_status launch(Params &p, const void *a, const void *b, cudaStream_t s) {
          tma_map_bf16(&tb, b, 2, (uint64_t)p.K, (uint64_t)p.rows, 1, BK);
   }
   if (!ok) return MOE_ERR_CUDA;
-  p.m_blocks = (p.N + C::TILE_M - 1) / C::TILE_M;
-  p.n_blocks = (p.K + BT - 1) / BT;
-  const long used = p.rows < p.E ? p.rows : p.E;  // groups with rows
-  const long tiles = MODE == TN ? (long)p.E * p.m_blocks * p.n_blocks
-                                : ((long)(p.rows + BT - 1) / BT + used) * p.m_blocks;  // at most
-  if (tiles > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
   const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart + kStaging;
   auto kern = grouped_gemm<MODE, BT>;
   static std::atomic<uint64_t> known[kMaxDevices];
   Launch l;
   const moe_status st = prepare_launch(kern, kThreads<MODE>, smem, C::PAIR, known, l);
   if (st != MOE_OK) return st;
-  if (!C::PAIR) {
-    kern<<<(int)(tiles < l.sms ? tiles : l.sms), kThreads<MODE>, smem, s>>>(ta, tb, p);
-  } else {
-    cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    lc.gridDim = dim3((unsigned)(2 * (tiles < l.pairs ? tiles : l.pairs)));
-    lc.blockDim = dim3(kThreads<MODE>);
-    lc.dynamicSmemBytes = smem;
-    lc.stream = s;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    MOE_CUDA_TRY(cudaLaunchKernelEx(&lc, kern, ta, tb, p));
-  }
+
+  p.m_blocks = (p.N + C::TILE_M - 1) / C::TILE_M;
+  const long used = p.rows < p.E ? p.rows : p.E;  // groups that can have rows
+  const long units = C::PAIR ? l.pairs : l.sms;
+  // tiles when all used groups are alike
+  auto tiles_of = [&](long tile) {
+    if (MODE == TN) return (long)p.E * p.m_blocks * ((p.K + tile - 1) / tile);
+    const long t = (p.rows + tile - 1) / tile;
+    return (t > used ? t : used) * p.m_blocks;
+  };
+  // Few tiles: narrower ones, then the reduction cut into parts (at least four
+  // blocks each), as long as they all run at once.
+  p.tile = BT;
+  while (p.tile > 64 && tiles_of(p.tile / 2) <= units) p.tile /= 2;
+  const long blocks = ((MODE == TN ? p.rows / used : p.K) + BK - 1) / BK;
+  const int most = C::PAIR ? 4 : 8;  // CTAs of a cluster: 8
+  p.split = 1;
+  while (p.split < most && tiles_of(p.tile) * p.split * 2 <= units && blocks >= p.split * 8) p.split *= 2;
+  p.n_blocks = (p.K + p.tile - 1) / p.tile;
+  const long tiles =
+      MODE == TN ? tiles_of(p.tile) : ((long)(p.rows + p.tile - 1) / p.tile + used) * p.m_blocks;  // at most
+  if (tiles > INT_MAX / 8) return MOE_ERR_UNSUPPORTED;
+  const int csize = (C::PAIR ? 2 : 1) * p.split;
+  // split: a cluster a tile; else every CTA or pair that fits walks the tiles
+  const long grid = p.split > 1 ? tiles * csize : (tiles < units ? tiles : units) * csize;
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)csize;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.gridDim = dim3((unsigned)grid);
+  lc.blockDim = dim3(kThreads<MODE>);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = csize > 1 ? 1 : 0;
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&lc, kern, ta, tb, p));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }

@@ -83,6 +83,8 @@ static_assert(sizeof(Smem<8>) <= kSmemPart, "barriers and tile list");
 
 struct Params {
   int rows, N, K, E, m_blocks;
+  int tile;   // tokens of a tile, at most BT
+  int split;  // parts that a tile's reduction is cut into, one a CTA of a cluster
   const int32_t *offsets;
   const uint8_t *sa, *sw;     // scale rows, for the path without TMA
   const float *ra, *rw;       // row scales [rows], [E, N], or null
@@ -145,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *stage_sb = stage_sa + STAGES * C::SA_BYTES;
   Smem<STAGES> &sm = *reinterpret_cast<Smem<STAGES> *>(stage_sb + STAGES * C::SB_BYTES);
 
+  float *parts = reinterpret_cast<float *>(base);  // split: over the stages once the MMAs have read them
   uint8_t *staging = reinterpret_cast<uint8_t *>(&sm) + kSmemPart;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_relinquish();
   }
   if (warp == 2) {
-    const bool ok = scan_tiles(p.offsets, p.rows, p.E, BT, sm.start);
+    const bool ok = scan_tiles(p.offsets, p.rows, p.E, p.tile, sm.start);
     if (kChecked && !ok && lane == 0 && blockIdx.x == 0) note_violation();
   }
   ptx::tc_fence_before();
@@ -186,7 +189,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem_base = sm.tmem_base;
   const int total = sm.start[p.E] * p.m_blocks;
-  const int kbs = (p.K + BK - 1) / BK;
+  // a cluster's CTAs share a tile, each with its blocks [kb0, kb1) of the reduction
+  const int part = (int)ptx::cluster_ctarank();
+  const int unit = (int)blockIdx.x / p.split, n_units = (int)gridDim.x / p.split;
+  const int blocks = (p.K + BK - 1) / BK;
+  const int kb0 = (int)((long)blocks * part / p.split), kb1 = (int)((long)blocks * (part + 1) / p.split);
   auto tile_of = [&](int t) { return token_tile(sm.start, p.offsets, p.rows, p.E, p.m_blocks, t, 16); };
 
   if (warp == 0) {
@@ -195,11 +202,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<STAGES> ring;
       uint32_t issued = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      for (int t = unit; t < total && ok; t += n_units) {
         const TokenTile tl = tile_of(t);
         const int boxes = (tl.count + TOK_BOX - 1) / TOK_BOX;
         const uint32_t tx = C::A_BYTES + boxes * TOK_BOX * ROW + (SF_TMA ? C::SA_BYTES + boxes * TOK_BOX * 16 : 0);
-        for (int kb = 0; kb < kbs; ++kb, ring.next(), ++issued) {
+        for (int kb = kb0; kb < kb1; ++kb, ring.next(), ++issued) {
           if (!wait_bar(&sm.empty[ring.s], ring.ph ^ 1u, &sm.abort, p.status)) {
             ok = false;
             break;
@@ -234,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ready = false, sf_ready = false;  // the next stage's barriers, read ahead
       int i = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++i) {
+      for (int t = unit; t < total && ok; t += n_units, ++i) {
         const TokenTile tl = tile_of(t);
         const int acc = i & 1;
         const uint32_t aph = (i >> 1) & 1u;
@@ -242,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BT;
         const uint32_t idesc = kIdesc0 | (uint32_t)((tl.count + 15) >> 4) << 18;  // N >> 3 at bit 17
-        for (int kb = 0; kb < kbs; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if ((!ready && !wait_bar(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) ||
               (!sf_ready && !wait_bar(&sm.sf_full[sf.s], sf.ph, &sm.abort, p.status))) {
             ok = false;
@@ -260,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < STEPS; ++k)
             mma_nvfp4(d_tmem, ad + k * (MMA_K / 2 >> 4), bd + k * (MMA_K / 2 >> 4), idesc, sfa + k * (BM / 32),
-                      sfb + k * (BT / 32), (kb | k) != 0);
+                      sfb + k * (BT / 32), ((kb - kb0) | k) != 0);
           ptx::mma_commit(&sm.empty[ring.s]);
           ptx::mma_commit(&sm.sf_empty[sf.s]);
           ring = nx;
@@ -281,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<STAGES> ring;
     Ring<2> sf;
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int t = unit; t < total && ok; t += n_units) {
       const TokenTile tl = tile_of(t);
       uint32_t va[AR][4], vb[BR][4];
       auto fetch = [&](int kb) {  // the path without TMA
@@ -297,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_scales(p.sa + (long)(tl.row0 + r) * pitch + kb * 16, r < tl.count ? left : 0, words, vb[j]);
         }
       };
-      if (!SF_TMA) fetch(0);
-      for (int kb = 0; kb < kbs; ++kb, ring.next(), sf.next()) {
+      if (!SF_TMA) fetch(kb0);
+      for (int kb = kb0; kb < kb1; ++kb, ring.next(), sf.next()) {
         if (SF_TMA) {
           if (!warp_wait(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) {
             ok = false;
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < C::SFA_COLS; c += 8) tmem_st8(at + c, ca + c);
 #pragma unroll
         for (int c = 0; c < C::SFB_COLS; c += 8) tmem_st8(at + C::SFA_COLS + c, cb + c);
-        if (!SF_TMA && kb + 1 < kbs) fetch(kb + 1);
+        if (!SF_TMA && kb + 1 < kb1) fetch(kb + 1);
         tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
     const RowStore store = {p.out, p.out_f32, p.N, p.ra, p.row_weight};
     int i = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x, ++i) {
+    for (int t = unit; t < total; t += n_units, ++i) {
       const TokenTile tl = tile_of(t);
       const int acc = i & 1;
       const uint32_t aph = (i >> 1) & 1u;
@@ -358,16 +365,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!epi_all(warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status))) break;
       ptx::tc_fence_after();
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
-      store_tokens(store, tbase, tl.row0, tl.count, tl.blk * BM, q, wn, staging, sm.wbuf + q * 32);
+      if (p.split > 1) put_part(parts, tbase, tl.count, q);
+      else store_tokens(store, tbase, tl.row0, tl.count, tl.blk * BM, q, wn, staging, sm.wbuf + q * 32);
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.tmem_empty[acc]);
     }
   }
 
+  if (p.split > 1) {
+    // the parts' sums, in the parts' order, each part a share of the tokens
+    __syncwarp();
+    ptx::cluster_sync();
+    if (unit < total) {
+      const TokenTile tl = tile_of(unit);
+      const int c_lo = tl.count * part / p.split, w = tl.count * (part + 1) / p.split - c_lo;
+      for (int i = threadIdx.x; i < w * BM; i += kThreads) {
+        const int f = i % BM, c = c_lo + i / BM, n = tl.blk * BM + f, r = tl.row0 + c;
+        if (n >= p.N) continue;
+        float sum = 0.0f;
+        for (int k = 0; k < p.split; ++k) sum += ld_part(parts + c * kPartPitch + f, (uint32_t)k);
+        if (p.rw) sum *= p.rw[(long)tl.e * p.N + n];
+        float rs = p.ra ? p.ra[r] : 1.0f;
+        if (p.row_weight) rs *= p.row_weight[r];
+        put_out(p.out, p.out_f32, (long)r * p.N + n, sum * rs, false);
+      }
+    }
+  }
   ptx::tc_fence_before();
   __syncwarp();
-  __syncthreads();
+  if (p.split > 1) ptx::cluster_sync();  // no CTA leaves while another reads its sums
+  else __syncthreads();
   if (warp == 1) {
     __syncwarp();
     ptx::tc_fence_after();
@@ -387,17 +415,40 @@ moe_status launch(Params &p, const void *a, const void *w, cudaStream_t s) {
   if (SF_TMA && (!tma_map_u8(&tsa, p.sw, (uint64_t)p.K / 16, p.N, p.E, 16, BM) ||
                  !tma_map_u8(&tsb, p.sa, (uint64_t)p.K / 16, p.rows, 1, 16, TOK_BOX)))
     return MOE_ERR_CUDA;
-  p.m_blocks = (p.N + BM - 1) / BM;
-  const long used = p.rows < p.E ? p.rows : p.E;
-  const long tiles = ((long)(p.rows + BT - 1) / BT + used) * p.m_blocks;
-  if (tiles > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
   const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart + kRowStage;
   auto kern = grouped_gemm_fp4<BT, SF_TMA>;
   static std::atomic<uint64_t> known[kMaxDevices];
   Launch l;
   const moe_status st = prepare_launch(kern, kThreads, smem, false, known, l);
   if (st != MOE_OK) return st;
-  kern<<<(int)(tiles < l.sms ? tiles : l.sms), kThreads, smem, s>>>(ta, tb, tsa, tsb, p);
+
+  p.m_blocks = (p.N + BM - 1) / BM;
+  const long used = p.rows < p.E ? p.rows : p.E;
+  // tiles when all used groups are alike; few: narrower, then cut (gemm_grouped.cu)
+  auto tiles_of = [&](long tile) {
+    const long t = (p.rows + tile - 1) / tile;
+    return (t > used ? t : used) * p.m_blocks;
+  };
+  p.tile = BT;
+  while (p.tile > 64 && tiles_of(p.tile / 2) <= l.sms) p.tile /= 2;
+  const int blocks = (p.K + BK - 1) / BK;
+  p.split = 1;
+  while (p.split < 8 && tiles_of(p.tile) * p.split * 2 <= l.sms && blocks >= p.split * 4) p.split *= 2;
+  const long tiles = ((long)(p.rows + p.tile - 1) / p.tile + used) * p.m_blocks;  // at most
+  if (tiles > INT_MAX / 8) return MOE_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : tiles < l.sms ? tiles : l.sms));
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = p.split > 1 ? 1 : 0;
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&lc, kern, ta, tb, tsa, tsb, p));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }

@@ -233,6 +233,40 @@ struct RowStore {
   const float *w0, *w1;  // factors of a row [rows], or null
 };
 
+// ---------------------------------------------------------------- split sums
+// A tile whose reduction is cut into parts: every part's CTA leaves its sums in
+// its shared memory, column by column (pitch 129: neighbouring columns of a
+// feature lie in different banks), and the CTAs of the cluster add them.
+constexpr int kPartPitch = 129;
+
+__device__ __forceinline__ void put_part(float *parts, uint32_t tbase, int count, int q) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int c = 0; c < count; c += 32) {
+    uint32_t v[32];
+    ptx::tmem_ld32(tbase + c, v);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (c + j < count) parts[(c + j) * kPartPitch + q * 32 + lane] = __uint_as_float(v[j]);
+  }
+}
+// The float at this address of shared memory in CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_part(const float *p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ptx::map_to_rank(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void put_out(void *out, int out_f32, long at, float v, bool accumulate) {
+  if (out_f32) {
+    float *o = (float *)out + at;
+    *o = accumulate ? *o + v : v;
+  } else {
+    __nv_bfloat16 *o = (__nv_bfloat16 *)out + at;
+    *o = __float2bfloat16_rn(accumulate ? __bfloat162float(*o) + v : v);
+  }
+}
+
 // q: this warp's lane quadrant; n0: the tile's first feature; scale: this
 // lane's feature factor.  stage: kRowStage bytes shared by the four warps;
 // wbuf: 32 floats of this warp's.

@@ -58,6 +58,10 @@ SIZES = {
     "edges": [0, 1, 15, 16, 17, 0, 63, 64, 65, 0],
     "wide": [255, 256, 257, 0, 300, 1],
     "few_of_many": [0] * 5 + [1, 0, 0, 2] + [0] * 30 + [1],
+    "long": [1501],                  # one group: its few tiles' reductions are cut into parts
+    "two_long": [300, 0, 419],
+    "many": [900, 37, 1500, 64, 0, 1030],    # more tiles than the GPU runs at once
+    "many_small": [(7 * i) % 23 for i in range(45)],
 }
 
 
@@ -67,7 +71,9 @@ SIZES = {
 @pytest.mark.parametrize("transposed", [False, True])
 @pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
 @pytest.mark.parametrize("sizes,N,K", [("one", 8, 8), ("one", 520, 4104), ("edges", 136, 72), ("edges", 384, 512),
-                                       ("wide", 128, 64), ("wide", 264, 200), ("few_of_many", 72, 1032)])
+                                       ("wide", 128, 64), ("wide", 264, 200), ("few_of_many", 72, 1032),
+                                       ("two_long", 264, 2056), ("long", 136, 1096), ("many", 2048, 136),
+                                       ("many_small", 640, 200)])
 def test_matmul(B, sizes, N, K, dtype, out, transposed):
     sizes = SIZES[sizes]
     E, dead = len(sizes), 5
@@ -113,7 +119,8 @@ def test_matmul_keeps_nan_and_infinity_to_their_rows(B, dtype):
 @pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("sizes,N,K", [("one", 8, 8), ("edges", 136, 72), ("edges", 128, 520), ("wide", 264, 200),
-                                       ("few_of_many", 72, 264)])
+                                       ("few_of_many", 72, 264), ("long", 136, 264), ("two_long", 72, 520),
+                                       ("many", 1000, 1032), ("many_small", 264, 136)])
 def test_wgrad(B, sizes, N, K, dtype, out, accumulate):
     sizes = SIZES[sizes]
     offs = _offsets(sizes, first=3)
@@ -178,7 +185,8 @@ def _nvfp4(seed, shape, scale=1.0):
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("sizes,N,K", [("one", 8, 32), ("one", 520, 4096), ("edges", 136, 96), ("edges", 128, 256),
                                        ("edges", 264, 832), ("wide", 200, 512), ("wide", 72, 288), ("wide", 256, 320),
-                                       ("few_of_many", 72, 1280)])
+                                       ("few_of_many", 72, 1280), ("two_long", 136, 4064), ("long", 128, 8192),
+                                       ("many", 1024, 512), ("many_small", 640, 544)])
 def test_matmul_nvfp4(B, sizes, N, K, out):
     sizes = SIZES[sizes]
     E, dead = len(sizes), 4
