@@ -89,8 +89,9 @@ struct Smem {
   uint32_t tmem_base;
   int abort;
   int start[MAX_E + 1];
+  int off[MAX_E + 1];
 };
-constexpr int kSmemPart = 5120;             // barriers and tile list
+constexpr int kSmemPart = 9216;             // barriers and tile list
 constexpr int kStaging = 4 * 32 * 32 * 4;   // epilogue: 4 KB a warp (TN), or two buffers of 32 tokens
 static_assert(kStaging == kRowStage, "one size for both epilogues");
 static_assert(sizeof(Smem<8>) <= kSmemPart, "the epilogue staging follows the barriers and tile list");
@@ -184,10 +185,12 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       ptx::tmem_relinquish();
     }
   }
-  if (warp == 2) {
+  load_offsets(p.offsets, p.rows, p.E, sm.off);
+  __syncthreads();
+  if (warp == 2 && (MODE != TN || kChecked)) {
     // TN needs no tile list (every group has m_blocks * n_blocks tiles), but
     // the same check of the offsets
-    const bool ok = scan_tiles(p.offsets, p.rows, p.E, p.tile, sm.start);
+    const bool ok = scan_tiles(sm.off, p.E, p.tile, sm.start);
     if (kChecked && !ok && lane == 0 && blockIdx.x == 0) note_violation();
     if (kChecked && MODE == TN && lane == 0) sm.start[0] = ok ? 0 : 1;
   }
@@ -222,11 +225,10 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       r.c0 = nb * p.tile;
       r.count = p.K - r.c0 < p.tile ? p.K - r.c0 : p.tile;
       r.row0 = 0;
-      r.k0 = seg_begin(p.offsets, p.rows, r.e);
-      r.red = seg_end(p.offsets, p.rows, r.e) - r.k0;
-      if (r.red < 0) r.red = 0;
+      r.k0 = sm.off[r.e];
+      r.red = group_rows(sm.off, r.e);
     } else {
-      const TokenTile tt = token_tile(sm.start, p.offsets, p.rows, p.E, p.m_blocks, t, C::N_STEP);
+      const TokenTile tt = token_tile(sm.start, sm.off, p.E, p.m_blocks, t, C::N_STEP);
       r.e = tt.e;
       r.m0 = tt.blk * C::TILE_M;
       r.c0 = 0;
@@ -437,7 +439,12 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       }
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
       if (p.split > 1) {
-        if (have) put_part(parts, tbase, tl.count, q);
+        if (!have) {
+        } else if (MODE != TN) {
+          put_part_columns(parts, tbase, tl.count, q);
+        } else {
+          put_part_features(parts, tbase, tl.count, p.tile + 4, q);
+        }
       } else if (MODE != TN) {
         store_tokens(store, tbase, tl.row0, tl.count, tl.m0 + (int)rank * BM, q, 1.0f,
                      reinterpret_cast<uint8_t *>(staging), sm.wbuf + q * 32);
@@ -561,20 +568,36 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     ptx::cluster_sync();
     if (unit < total) {
       const Tile tl = tile_of(unit);
-      const int c_lo = tl.count * part / p.split, w = tl.count * (part + 1) / p.split - c_lo;
       const int n0 = tl.m0 + (int)rank * BM;
-      for (int i = threadIdx.x; i < w * BM; i += kThreads<MODE>) {
-        const int f = MODE == TN ? i / w : i % BM, c = c_lo + (MODE == TN ? i - f * w : i / BM);
-        if (n0 + f >= p.N) continue;
-        float sum = 0.0f;
-        for (int k = 0; k < p.split; ++k)
-          if (tl.first_block(k, p.split) < tl.first_block(k + 1, p.split))
-            sum += ld_part(parts + c * kPartPitch + f, PAIR ? 2 * k + rank : (uint32_t)k);
-        if (MODE != TN) {
-          if (p.row_weight) sum *= p.row_weight[tl.row0 + c];
-          put_out(p.out, p.out_f32, (long)(tl.row0 + c) * p.N + n0 + f, sum, false);
-        } else if (tl.blocks > 0 || !p.accumulate) {
-          put_out(p.out, p.out_f32, ((long)tl.e * p.N + n0 + f) * p.K + tl.c0 + c, sum, p.accumulate != 0);
+      uint32_t has = 0;  // parts with something to add
+      for (int k = 0; k < p.split; ++k)
+        if (tl.first_block(k, p.split) < tl.first_block(k + 1, p.split)) has |= 1u << k;
+      constexpr uint32_t step = PAIR ? 2 : 1;
+      if (MODE != TN) {
+        const int c_lo = tl.count * part / p.split, w = tl.count * (part + 1) / p.split - c_lo;
+        const RowStore store = {p.out, p.out_f32, p.N, p.row_weight, nullptr};
+        store_summed_tokens(store, parts, tl.row0, c_lo, w, n0, nullptr, rank, step, p.split, has, kThreads<MODE>);
+      } else if (has || !p.accumulate) {
+        constexpr int U = 4;
+        const int quads = tl.count / 4;                                      // of a row
+        const int f_lo = BM * part / p.split, rows = BM / p.split;            // split: a power of two
+        const int all = rows * quads;
+        for (int i0 = threadIdx.x; i0 < all; i0 += U * kThreads<MODE>) {
+          int at[U];
+          float4 sum[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u * kThreads<MODE>, all - 1), f = i / quads;
+            at[u] = (f_lo + f) * (p.tile + 4) + (i - f * quads) * 4;
+          }
+          add_parts(parts, at, rank, step, p.split, has, sum);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * kThreads<MODE>, f = i / quads, n = n0 + f_lo + f;
+            if (i < all && n < p.N)
+              put_quad(p.out, p.out_f32, ((long)tl.e * p.N + n) * p.K + tl.c0 + (i - f * quads) * 4, sum[u],
+                       p.accumulate != 0);
+          }
         }
       }
     }
@@ -623,14 +646,17 @@ moe_status launch(Params &p, const void *a, const void *b, cudaStream_t s) {
     const long t = (p.rows + tile - 1) / tile;
     return (t > used ? t : used) * p.m_blocks;
   };
-  // Few tiles: narrower ones, then the reduction cut into parts (at least four
-  // blocks each), as long as they all run at once.
+  // Few tiles: narrower ones, then the reduction cut into parts, as long as they
+  // all run at once.  A block takes about 0.2 us when few CTAs run, the cluster
+  // and its sum 2.5 us (200 rows x 512 x 128: 5.9 us whole, 8.4 in two parts;
+  // 1 row x 14336 x 4096: 49 us whole, 28 in four): cut from 32 blocks on, into
+  // parts of at least eight.
   p.tile = BT;
   while (p.tile > 64 && tiles_of(p.tile / 2) <= units) p.tile /= 2;
   const long blocks = ((MODE == TN ? p.rows / used : p.K) + BK - 1) / BK;
   const int most = C::PAIR ? 4 : 8;  // CTAs of a cluster: 8
   p.split = 1;
-  while (p.split < most && tiles_of(p.tile) * p.split * 2 <= units && blocks >= p.split * 8) p.split *= 2;
+  while (p.split < most && tiles_of(p.tile) * p.split * 2 <= units && blocks >= 32 && blocks >= p.split * 16) p.split *= 2;
   p.n_blocks = (p.K + p.tile - 1) / p.tile;
   const long tiles =
       MODE == TN ? tiles_of(p.tile) : ((long)(p.rows + p.tile - 1) / p.tile + used) * p.m_blocks;  // at most

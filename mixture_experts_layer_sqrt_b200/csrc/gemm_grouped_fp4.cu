@@ -59,17 +59,18 @@ struct Cfg {
   static constexpr int SFA_COLS = STEPS * BM / 32;   // TMEM columns of a stage's scales
   static constexpr int SFB_COLS = STEPS * BT / 32;
   static constexpr int SF_COLS = SFA_COLS + SFB_COLS;
+  static constexpr int SF_BUFS = BT == 192 ? 3 : 4;  // stages' scales in TMEM at once
   static constexpr int SF_BASE = 2 * BT;             // past the two accumulators
   static constexpr uint32_t TMEM_COLS = BT == 192 ? 512 : 256;
-  static_assert(SF_BASE + 2 * SF_COLS <= (int)TMEM_COLS, "accumulators and scales fit in TMEM");
+  static_assert(SF_BASE + SF_BUFS * SF_COLS <= (int)TMEM_COLS, "accumulators and scales fit in TMEM");
 };
 
 template <int STAGES>
 struct Smem {
   uint64_t full[STAGES];
   uint64_t empty[STAGES];
-  uint64_t sf_full[2];
-  uint64_t sf_empty[2];
+  uint64_t sf_full[4];
+  uint64_t sf_empty[4];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint64_t drain;
@@ -77,8 +78,9 @@ struct Smem {
   uint32_t tmem_base;
   int abort;
   int start[MAX_E + 1];
+  int off[MAX_E + 1];
 };
-constexpr int kSmemPart = 5120;
+constexpr int kSmemPart = 9216;
 static_assert(sizeof(Smem<8>) <= kSmemPart, "barriers and tile list");
 
 struct Params {
@@ -157,9 +159,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&sm.full[s], 1);
       ptx::mbar_init(&sm.empty[s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < C::SF_BUFS; ++a) {
       ptx::mbar_init(&sm.sf_full[a], 4);
       ptx::mbar_init(&sm.sf_empty[a], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&sm.tmem_full[a], 1);
       ptx::mbar_init(&sm.tmem_empty[a], 4);
     }
@@ -180,8 +184,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_alloc(&sm.tmem_base, C::TMEM_COLS);
     ptx::tmem_relinquish();
   }
+  load_offsets(p.offsets, p.rows, p.E, sm.off);
+  __syncthreads();
   if (warp == 2) {
-    const bool ok = scan_tiles(p.offsets, p.rows, p.E, p.tile, sm.start);
+    const bool ok = scan_tiles(sm.off, p.E, p.tile, sm.start);
     if (kChecked && !ok && lane == 0 && blockIdx.x == 0) note_violation();
   }
   ptx::tc_fence_before();
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int unit = (int)blockIdx.x / p.split, n_units = (int)gridDim.x / p.split;
   const int blocks = (p.K + BK - 1) / BK;
   const int kb0 = (int)((long)blocks * part / p.split), kb1 = (int)((long)blocks * (part + 1) / p.split);
-  auto tile_of = [&](int t) { return token_tile(sm.start, p.offsets, p.rows, p.E, p.m_blocks, t, 16); };
+  auto tile_of = [&](int t) { return token_tile(sm.start, sm.off, p.E, p.m_blocks, t, 16); };
 
   if (warp == 0) {
     // ================================================= TMA producer
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t ad0 = ptx::desc_kmajor_sw128(ptx::smem_addr(stage_a));
       const uint64_t bd0 = ptx::desc_kmajor_sw128(ptx::smem_addr(stage_b));
       Ring<STAGES> ring;
-      Ring<2> sf;
+      Ring<C::SF_BUFS> sf;
       bool ready = false, sf_ready = false;  // the next stage's barriers, read ahead
       int i = 0;
       bool ok = true;
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_fence_after();
           Ring<STAGES> nx = ring;
           nx.next();
-          Ring<2> sn = sf;
+          Ring<C::SF_BUFS> sn = sf;
           sn.next();
           ready = ptx::mbar_try_wait(&sm.full[nx.s], nx.ph);
           sf_ready = ptx::mbar_try_wait(&sm.sf_full[sn.s], sn.ph);
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool words = (p.K & 63) == 0;
     const int pitch = p.K / 16;
     Ring<STAGES> ring;
-    Ring<2> sf;
+    Ring<C::SF_BUFS> sf;
     bool ok = true;
     for (int t = unit; t < total && ok; t += n_units) {
       const TokenTile tl = tile_of(t);
@@ -365,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!epi_all(warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status))) break;
       ptx::tc_fence_after();
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
-      if (p.split > 1) put_part(parts, tbase, tl.count, q);
+      if (p.split > 1) put_part_columns(parts, tbase, tl.count, q);
       else store_tokens(store, tbase, tl.row0, tl.count, tl.blk * BM, q, wn, staging, sm.wbuf + q * 32);
       ptx::tc_fence_before();
       __syncwarp();
@@ -380,16 +386,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (unit < total) {
       const TokenTile tl = tile_of(unit);
       const int c_lo = tl.count * part / p.split, w = tl.count * (part + 1) / p.split - c_lo;
-      for (int i = threadIdx.x; i < w * BM; i += kThreads) {
-        const int f = i % BM, c = c_lo + i / BM, n = tl.blk * BM + f, r = tl.row0 + c;
-        if (n >= p.N) continue;
-        float sum = 0.0f;
-        for (int k = 0; k < p.split; ++k) sum += ld_part(parts + c * kPartPitch + f, (uint32_t)k);
-        if (p.rw) sum *= p.rw[(long)tl.e * p.N + n];
-        float rs = p.ra ? p.ra[r] : 1.0f;
-        if (p.row_weight) rs *= p.row_weight[r];
-        put_out(p.out, p.out_f32, (long)r * p.N + n, sum * rs, false);
-      }
+      const RowStore store = {p.out, p.out_f32, p.N, p.ra, p.row_weight};
+      store_summed_tokens(store, parts, tl.row0, c_lo, w, tl.blk * BM, p.rw ? p.rw + (long)tl.e * p.N : nullptr, 0, 1,
+                          p.split, (1u << p.split) - 1, kThreads);
     }
   }
   ptx::tc_fence_before();
@@ -433,7 +432,7 @@ moe_status launch(Params &p, const void *a, const void *w, cudaStream_t s) {
   while (p.tile > 64 && tiles_of(p.tile / 2) <= l.sms) p.tile /= 2;
   const int blocks = (p.K + BK - 1) / BK;
   p.split = 1;
-  while (p.split < 8 && tiles_of(p.tile) * p.split * 2 <= l.sms && blocks >= p.split * 4) p.split *= 2;
+  while (p.split < 8 && tiles_of(p.tile) * p.split * 2 <= l.sms && blocks >= 16 && blocks >= p.split * 8) p.split *= 2;
   const long tiles = ((long)(p.rows + p.tile - 1) / p.tile + used) * p.m_blocks;  // at most
   if (tiles > INT_MAX / 8) return MOE_ERR_UNSUPPORTED;
   cudaLaunchConfig_t lc = {};

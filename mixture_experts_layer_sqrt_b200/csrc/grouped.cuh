@@ -121,48 +121,55 @@ struct Ring {
   }
 };
 
-// Rows [begin, end) of group e, kept within [0, rows] whatever the offsets
-// hold, so that offsets out of range cannot lead to an access out of range.
-// offsets == null: one group of all rows.
-__device__ __forceinline__ int clamp_row(int v, int rows) { return v < 0 ? 0 : (v > rows ? rows : v); }
-__device__ __forceinline__ int seg_begin(const int32_t *offsets, int rows, int e) {
-  return offsets ? clamp_row(offsets[e], rows) : 0;
+// Group offsets to shared memory, off[0..E], by all threads of the block (then a
+// barrier): one load latency whatever E, where a warp that scanned them from
+// global memory took 10 us for 384 groups.  They are kept within [0, rows], so
+// that offsets out of range cannot lead to an access out of range.  offsets ==
+// null: one group of all rows.  Checked build: a negative or decreasing offset
+// leaves all groups empty (scan_tiles).
+__device__ __forceinline__ void load_offsets(const int32_t *offsets, int rows, int E, int *off) {
+#pragma unroll 4
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+    const int v = offsets ? offsets[e] : (e ? rows : 0);
+    off[e] = kChecked ? (v > rows ? rows : v) : (v < 0 ? 0 : (v > rows ? rows : v));
+  }
 }
-__device__ __forceinline__ int seg_end(const int32_t *offsets, int rows, int e) {
-  return offsets ? clamp_row(offsets[e + 1], rows) : rows;
+// Rows of group e; 0 if the offsets decrease.
+__device__ __forceinline__ int group_rows(const int *off, int e) {
+  const int n = off[e + 1] - off[e];
+  return n > 0 ? n : 0;
 }
 
 // One warp: start[e] = sum over e' < e of ceil(rows_e' / tile_rows), e = 0..E
-// (the last entry is the total).  Checked build: false if an offset is below
-// 0 or the offsets decrease, and then every group counts as empty.
-__device__ __forceinline__ bool scan_tiles(const int32_t *offsets, int rows, int E, int tile_rows, int *start) {
+// (the last entry is the total).  Checked build: false if the offsets are bad.
+__device__ __forceinline__ bool scan_tiles(int *off, int E, int tile_rows, int *start) {
   const int lane = threadIdx.x & 31;
-  int carry = 0;
-  bool bad = false;
-  for (int e0 = 0; e0 < E; e0 += 32) {
-    const int e = e0 + lane;
-    int v = 0;
-    if (e < E) {
-      const int n = seg_end(offsets, rows, e) - seg_begin(offsets, rows, e);
-      if (kChecked && offsets && (offsets[e] < 0 || offsets[e + 1] < offsets[e])) bad = true;
-      v = n > 0 ? (n + tile_rows - 1) / tile_rows : 0;
+  if (kChecked) {
+    bool bad = false;
+    for (int e = lane; e < E; e += 32) bad |= off[e] < 0 || off[e + 1] < off[e];
+    if (__any_sync(0xffffffffu, bad)) {
+      for (int e = lane; e <= E; e += 32) off[e] = start[e] = 0;
+      return false;
     }
-    int incl = v;
+  }
+  // a lane's groups in a row, then one scan over the lanes
+  const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
+  int sum = 0;
+#pragma unroll 4
+  for (int e = e0; e < e1; ++e) {
+    start[e] = sum;
+    sum += (group_rows(off, e) + tile_rows - 1) / tile_rows;
+  }
+  int incl = sum;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
-    }
-    if (e < E) start[e] = carry + incl - v;
-    carry += __shfl_sync(0xffffffffu, incl, 31);
+  for (int s = 1; s < 32; s <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, s);
+    if (lane >= s) incl += o;
   }
-  const bool any_bad = kChecked && __any_sync(0xffffffffu, bad);
-  if (any_bad) {
-    for (int e = lane; e < E; e += 32) start[e] = 0;
-    carry = 0;
-  }
-  if (lane == 0) start[E] = carry;
-  return !any_bad;
+#pragma unroll 4
+  for (int e = e0; e < e1; ++e) start[e] += incl - sum;
+  if (lane == 31) start[E] = incl;
+  return true;
 }
 
 // Largest e with start[e] * per <= t (empty groups share the next start).
@@ -183,18 +190,17 @@ __device__ __forceinline__ int find_group(const int *start, int E, int per, int 
 struct TokenTile {
   int e, blk, row0, count;  // group, output-feature block, first row, rows
 };
-__device__ __forceinline__ TokenTile token_tile(const int *start, const int32_t *offsets, int rows, int E, int blocks,
-                                                int t, int step) {
+__device__ __forceinline__ TokenTile token_tile(const int *start, const int *off, int E, int blocks, int t, int step) {
   TokenTile r;
   r.e = find_group(start, E, blocks, t);
   const int tiles = start[r.e + 1] - start[r.e];
   const int local = t - start[r.e] * blocks;
   r.blk = local / tiles;
   const int j = local - r.blk * tiles;
-  const int begin = seg_begin(offsets, rows, r.e), end = seg_end(offsets, rows, r.e);
-  const int width = ((end - begin + tiles - 1) / tiles + step - 1) & ~(step - 1);
+  const int begin = off[r.e], n = group_rows(off, r.e);
+  const int width = ((n + tiles - 1) / tiles + step - 1) & ~(step - 1);
   r.row0 = begin + j * width;
-  r.count = end - r.row0 < width ? end - r.row0 : width;
+  r.count = n - j * width < width ? n - j * width : width;
   return r;
 }
 
@@ -235,11 +241,14 @@ struct RowStore {
 
 // ---------------------------------------------------------------- split sums
 // A tile whose reduction is cut into parts: every part's CTA leaves its sums in
-// its shared memory, column by column (pitch 129: neighbouring columns of a
-// feature lie in different banks), and the CTAs of the cluster add them.
-constexpr int kPartPitch = 129;
+// its shared memory and the CTAs of the cluster add them, in the parts' order,
+// four neighbours of the output a thread, several quads' loads in flight (one
+// load after the other took 10 us for 64 x 128 sums of two parts, this 1-2).
+//   by column  [column][feature], pitch 132: tokens x features
+//   by feature [feature][column], pitch columns + 4: rows of dW
+constexpr int kColPitch = 132;
 
-__device__ __forceinline__ void put_part(float *parts, uint32_t tbase, int count, int q) {
+__device__ __forceinline__ void put_part_columns(float *parts, uint32_t tbase, int count, int q) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int c = 0; c < count; c += 32) {
@@ -248,22 +257,96 @@ __device__ __forceinline__ void put_part(float *parts, uint32_t tbase, int count
     ptx::tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (c + j < count) parts[(c + j) * kPartPitch + q * 32 + lane] = __uint_as_float(v[j]);
+      if (c + j < count) parts[(c + j) * kColPitch + q * 32 + lane] = __uint_as_float(v[j]);
   }
 }
-// The float at this address of shared memory in CTA `rank` of the cluster.
-__device__ __forceinline__ float ld_part(const float *p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ptx::map_to_rank(p, rank)) : "memory");
-  return v;
+__device__ __forceinline__ void put_part_features(float *parts, uint32_t tbase, int count, int pitch, int q) {
+  float *row = parts + (q * 32 + (threadIdx.x & 31)) * pitch;
+#pragma unroll 1
+  for (int c = 0; c < count; c += 32) {
+    uint32_t v[32];
+    ptx::tmem_ld32(tbase + c, v);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; j += 4)
+      if (c + j < count) *reinterpret_cast<uint4 *>(row + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+  }
 }
-__device__ __forceinline__ void put_out(void *out, int out_f32, long at, float v, bool accumulate) {
+
+// Sums of the quads at parts + at[u] over the CTAs first, first + step, ... of
+// the cluster (`n` of them, only those with `has` bit set), U quads at once.
+template <int U>
+__device__ __forceinline__ void add_parts(const float *parts, const int (&at)[U], uint32_t first, uint32_t step, int n,
+                                          uint32_t has, float4 (&sum)[U]) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) sum[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int k = 0; k < n; ++k) {
+    if (!(has >> k & 1)) continue;
+    const uint32_t base = ptx::map_to_rank(parts, first + k * step);
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[u].x), "=f"(v[u].y), "=f"(v[u].z), "=f"(v[u].w)
+                   : "r"(base + (uint32_t)at[u] * 4u));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      sum[u].x += v[u].x;
+      sum[u].y += v[u].y;
+      sum[u].z += v[u].z;
+      sum[u].w += v[u].w;
+    }
+  }
+}
+__device__ __forceinline__ void put_quad(void *out, int out_f32, long at, float4 v, bool accumulate) {
   if (out_f32) {
-    float *o = (float *)out + at;
-    *o = accumulate ? *o + v : v;
-  } else {
-    __nv_bfloat16 *o = (__nv_bfloat16 *)out + at;
-    *o = __float2bfloat16_rn(accumulate ? __bfloat162float(*o) + v : v);
+    float4 *o = reinterpret_cast<float4 *>((float *)out + at);
+    if (accumulate) {
+      const float4 old = *o;
+      v = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
+    }
+    *o = v;
+  } else {  // rounded once
+    uint2 *o = reinterpret_cast<uint2 *>((__nv_bfloat16 *)out + at);
+    if (accumulate) {
+      const uint2 old = *o;
+      const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&old.x));
+      const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&old.y));
+      v = make_float4(a.x + v.x, a.y + v.y, b.x + v.z, b.y + v.w);
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *o = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+  }
+}
+// This CTA's share of a tile of tokens: tokens [c_lo, c_lo + w) x 128 features from n0 on.
+__device__ __forceinline__ void store_summed_tokens(const RowStore &o, const float *parts, int row0, int c_lo, int w,
+                                                    int n0, const float *feature_scale, uint32_t first, uint32_t step,
+                                                    int n, uint32_t has, int threads) {
+  constexpr int U = 4;
+  const int quads = w * 32;
+  for (int i0 = threadIdx.x; i0 < quads; i0 += U * threads) {
+    int at[U];
+    float4 sum[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = min(i0 + u * threads, quads - 1);
+      at[u] = (c_lo + (i >> 5)) * kColPitch + (i & 31) * 4;
+    }
+    add_parts(parts, at, first, step, n, has, sum);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * threads, r = row0 + c_lo + (i >> 5), f = n0 + (i & 31) * 4;
+      if (i >= quads || f >= o.N) continue;
+      float4 v = sum[u];
+      if (feature_scale) {
+        const float *s = feature_scale + f;
+        v = make_float4(v.x * s[0], v.y * s[1], v.z * s[2], v.w * s[3]);
+      }
+      float k = 1.0f;
+      if (o.w0) k = o.w0[r];
+      if (o.w1) k *= o.w1[r];
+      put_quad(o.out, o.out_f32, (long)r * o.N + f, make_float4(v.x * k, v.y * k, v.z * k, v.w * k), false);
+    }
   }
 }
 
