@@ -142,7 +142,7 @@ def _expect(t: Optional[torch.Tensor], shape, dtype, what: str):
     """Buffers handed to the library must match what it will write."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{what}: expected contiguous {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -408,7 +408,7 @@ def grouped_matmul(a: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Ten
         with _on(d, stream):
             return grouped_matmul(a, w, offsets, transposed, row_weight, y, out, ws)
     if y is None:
-        y = torch.empty((rows, N), dtype=odt, device=a.device)
+        y = a.new_empty((rows, N), dtype=odt)
     if ws is None:
         ws = workspace(256, a.device)
     _check(lib.moe_grouped_matmul(g, _p(a), _p(offsets), _p(w), transposed, _p(row_weight), _p(y), _p(ws), ws.numel(),
@@ -439,7 +439,7 @@ def grouped_wgrad(dy: torch.Tensor, a: torch.Tensor, offsets: Optional[torch.Ten
         with _on(d, stream):
             return grouped_wgrad(dy, a, offsets, dw, accumulate, out, ws)
     if dw is None:
-        dw = torch.empty((E, N, K), dtype=odt, device=a.device)
+        dw = a.new_empty((E, N, K), dtype=odt)
     if ws is None:
         ws = workspace(256, a.device)
     _check(lib.moe_grouped_wgrad(g, _p(dy), _p(a), _p(offsets), accumulate, _p(dw), _p(ws), ws.numel(),
@@ -473,7 +473,7 @@ def grouped_matmul_nvfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
             return grouped_matmul_nvfp4(a, a_scales, w, w_scales, offsets, a_row_scale, w_row_scale, row_weight, y, out,
                                         ws)
     if y is None:
-        y = torch.empty((rows, N), dtype=odt, device=a.device)
+        y = a.new_empty((rows, N), dtype=odt)
     if ws is None:
         ws = workspace(256, a.device)
     _check(lib.moe_grouped_matmul_nvfp4(g, _p(a), _p(a_scales), _p(a_row_scale), _p(offsets), _p(w), _p(w_scales),
@@ -568,7 +568,7 @@ def swiglu(gu: torch.Tensor, clamp: float = 0.0, clamp_mode="preact", offsets: O
         with _on(d, stream):
             return swiglu(gu, clamp, clamp_mode, offsets, h)
     if h is None:
-        h = torch.empty((rows, F), dtype=gu.dtype, device=gu.device)
+        h = gu.new_empty((rows, F))
     _check(lib.moe_swiglu(rows, F, dt, _p(gu), clamp, CLAMP_MODES[clamp_mode], _live(offsets), _p(h), _raw_stream(d)),
            "moe_swiglu")
     return h
@@ -600,7 +600,7 @@ def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, row_weight: Optional[tor
     if hw is None and need_hw:
         hw = torch.empty_like(dh)
     if drw is None and need_drow_weight:
-        drw = torch.empty(rows, dtype=torch.float32, device=gu.device)
+        drw = gu.new_empty((rows,), dtype=torch.float32)
     _check(lib.moe_swiglu_backward(rows, F, dt, _p(gu), _p(dh), _p(row_weight), clamp, CLAMP_MODES[clamp_mode],
                                    _live(offsets), _p(dgu), _p(hw), _p(drw), _raw_stream(d)), "moe_swiglu_backward")
     return dict(dgu=dgu, hw=hw, drow_weight=drw)

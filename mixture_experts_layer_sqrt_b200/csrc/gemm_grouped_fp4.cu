@@ -10,20 +10,23 @@
 // Layout of the work as in gemm_grouped.cu: weights on the MMA's M side (128
 // output features a tile), the tokens of one group on its N side (up to BT,
 // rounded to 16), so ragged groups pad nothing and the packed weights are read
-// once per BT tokens.  A stage holds 256 reduction elements: rows of 128 bytes
-// of codes (128-byte swizzle) and 16 bytes of scales.
+// once per BT tokens.  A stage of codes holds 256 reduction elements, rows of
+// 128 bytes (128-byte swizzle); a stage of scales those of four of them, rows of
+// 64 bytes (64-byte swizzle).  TMA's cost is by the row here: 49152 rows x 4096
+// x 2048 over 384 groups took 418-427 us with 16 bytes of scales a row and
+// stage, 417 with 32, 399 with 64.
 //
 // The MMA takes the scales from TMEM: for each 64 reduction elements one
 // 32-bit column per 32 rows (lane i of column j: the four scale bytes of row
 // 32 j + i), the same in all four lane quadrants.  Four warps, one a quadrant,
-// copy them there from the stage with tcgen05.st, one 16-byte read a row, a
-// stage ahead of the MMAs (two TMEM buffers).  Scale rows that TMA cannot read
+// copy them there from the stage with tcgen05.st, one 16-byte read a row, up to
+// SF_BUFS stages ahead of the MMAs.  Scale rows that TMA cannot read
 // (K not a multiple of 256: rows not a multiple of 16 bytes) are loaded by the
 // same warps from global memory, one stage ahead in registers.
 //
-// Roles (320 threads, persistent, one CTA per SM): warp 0 TMA producer, warp 1
-// TMEM owner and MMA issuer, warps 2-5 epilogue, warps 6-9 scales.  Every wait
-// is bounded.
+// Roles (352 threads, persistent, one CTA per SM): warp 0 TMA producer of the
+// weights, warp 1 TMEM owner and MMA issuer, warps 2-5 epilogue, warps 6-9
+// scales, warp 10 TMA producer of the tokens.  Every wait is bounded.
 #include <cudaTypedefs.h>
 #include <limits.h>
 
@@ -45,17 +48,21 @@ constexpr int ROW = BK / 2;             // bytes of codes a row and stage
 constexpr int MMA_K = 64;
 constexpr int STEPS = BK / MMA_K;
 constexpr int TOK_BOX = 32;             // token rows per TMA box
-constexpr int kThreads = 320;
+constexpr int SPAN = 4;                 // stages of codes that a stage of scales covers
+constexpr int SROW = 16 * SPAN;         // its bytes a row
+constexpr int S_STAGES = 2;
+constexpr int kThreads = 352;
 constexpr int kScaleWarp0 = 6;
+constexpr int kTokenWarp = 10;
 
 template <int BT>
 struct Cfg {
-  static constexpr int A_BYTES = BM * ROW;
-  static constexpr int B_BYTES = BT * ROW;
-  static constexpr int SA_BYTES = BM * 16;
-  static constexpr int SB_BYTES = BT * 16;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
-  static constexpr int STAGES = BT == 192 ? 4 : 7;
+  static constexpr int A_BYTES = BM * ROW, B_BYTES = BT * ROW;  // codes of a stage
+  // Rings of their own: the weights come from DRAM, the tokens mostly from L2.
+  static constexpr int A_STAGES = BT == 192 ? 4 : 8;
+  static constexpr int B_STAGES = BT == 192 ? 4 : 5;
+  static constexpr int S_BYTES = (BM + BT) * SROW;              // scales of SPAN stages
+  static constexpr int BYTES = A_STAGES * A_BYTES + B_STAGES * B_BYTES + S_STAGES * S_BYTES;
   static constexpr int SFA_COLS = STEPS * BM / 32;   // TMEM columns of a stage's scales
   static constexpr int SFB_COLS = STEPS * BT / 32;
   static constexpr int SF_COLS = SFA_COLS + SFB_COLS;
@@ -65,10 +72,10 @@ struct Cfg {
   static_assert(SF_BASE + SF_BUFS * SF_COLS <= (int)TMEM_COLS, "accumulators and scales fit in TMEM");
 };
 
-template <int STAGES>
 struct Smem {
-  uint64_t full[STAGES];
-  uint64_t empty[STAGES];
+  uint64_t a_full[8], a_empty[8];                    // weight codes
+  uint64_t b_full[8], b_empty[8];                    // token codes
+  uint64_t s_full[S_STAGES], s_empty[S_STAGES];      // scales of both
   uint64_t sf_full[4];
   uint64_t sf_empty[4];
   uint64_t tmem_full[2];
@@ -81,7 +88,7 @@ struct Smem {
   int off[MAX_E + 1];
 };
 constexpr int kSmemPart = 9216;
-static_assert(sizeof(Smem<8>) <= kSmemPart, "barriers and tile list");
+static_assert(sizeof(Smem) <= kSmemPart, "barriers and tile list");
 
 struct Params {
   int rows, N, K, E, m_blocks;
@@ -140,24 +147,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                      const Params p) {
   using C = Cfg<BT>;
-  constexpr int STAGES = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *stage_a = base;
-  uint8_t *stage_b = stage_a + STAGES * C::A_BYTES;
-  uint8_t *stage_sa = stage_b + STAGES * C::B_BYTES;
-  uint8_t *stage_sb = stage_sa + STAGES * C::SA_BYTES;
-  Smem<STAGES> &sm = *reinterpret_cast<Smem<STAGES> *>(stage_sb + STAGES * C::SB_BYTES);
-
+  uint8_t *stage_b = stage_a + C::A_STAGES * C::A_BYTES;
+  uint8_t *stage_s = stage_b + C::B_STAGES * C::B_BYTES;  // rows of the weights, then of the tokens
+  Smem &sm = *reinterpret_cast<Smem *>(base + C::BYTES);
   float *parts = reinterpret_cast<float *>(base);  // split: over the stages once the MMAs have read them
   uint8_t *staging = reinterpret_cast<uint8_t *>(&sm) + kSmemPart;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      ptx::mbar_init(&sm.full[s], 1);
-      ptx::mbar_init(&sm.empty[s], 1);
+    for (int s = 0; s < C::A_STAGES; ++s) {
+      ptx::mbar_init(&sm.a_full[s], 1);
+      ptx::mbar_init(&sm.a_empty[s], 1);
+    }
+    for (int s = 0; s < C::B_STAGES; ++s) {
+      ptx::mbar_init(&sm.b_full[s], 1);
+      ptx::mbar_init(&sm.b_empty[s], 1);
+    }
+    for (int s = 0; s < S_STAGES; ++s) {
+      ptx::mbar_init(&sm.s_full[s], 2);   // both producers
+      ptx::mbar_init(&sm.s_empty[s], 4);  // scale warps
     }
     for (int a = 0; a < C::SF_BUFS; ++a) {
       ptx::mbar_init(&sm.sf_full[a], 4);
@@ -202,39 +214,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kb0 = (int)((long)blocks * part / p.split), kb1 = (int)((long)blocks * (part + 1) / p.split);
   auto tile_of = [&](int t) { return token_tile(sm.start, sm.off, p.E, p.m_blocks, t, 16); };
 
-  if (warp == 0) {
-    // ================================================= TMA producer
+  if (warp == 0 || warp == kTokenWarp) {
+    // ================================================= TMA producers: weights, tokens
+    const bool weights = warp == 0;
     if (elect_one()) {
-      Ring<STAGES> ring;
-      uint32_t issued = 0;
+      uint64_t *const full = weights ? sm.a_full : sm.b_full, *const empty = weights ? sm.a_empty : sm.b_empty;
+      const int stages = weights ? C::A_STAGES : C::B_STAGES;
+      int s = 0;
+      uint32_t ph = 0, issued = 0, s_issued = 0;
+      Ring<S_STAGES> sc;
       bool ok = true;
       for (int t = unit; t < total && ok; t += n_units) {
         const TokenTile tl = tile_of(t);
         const int boxes = (tl.count + TOK_BOX - 1) / TOK_BOX;
-        const uint32_t tx = C::A_BYTES + boxes * TOK_BOX * ROW + (SF_TMA ? C::SA_BYTES + boxes * TOK_BOX * 16 : 0);
-        for (int kb = kb0; kb < kb1; ++kb, ring.next(), ++issued) {
-          if (!wait_bar(&sm.empty[ring.s], ring.ph ^ 1u, &sm.abort, p.status)) {
+        const uint32_t tx = weights ? C::A_BYTES : boxes * TOK_BOX * ROW;
+        const uint32_t s_tx = weights ? BM * SROW : boxes * TOK_BOX * SROW;
+        for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+          if (SF_TMA && (kb - kb0) % SPAN == 0) {
+            if (!wait_bar(&sm.s_empty[sc.s], sc.ph ^ 1u, &sm.abort, p.status)) {
+              ok = false;
+              break;
+            }
+            uint8_t *d = stage_s + sc.s * C::S_BYTES;
+            ptx::mbar_arrive_expect_tx(&sm.s_full[sc.s], s_tx);
+            if (weights) {
+              ptx::tma_load_3d(d, &tmSA, &sm.s_full[sc.s], kb * 16, tl.blk * BM, tl.e);
+            } else {
+              for (int i = 0; i < boxes; ++i)
+                ptx::tma_load_3d(d + (BM + i * TOK_BOX) * SROW, &tmSB, &sm.s_full[sc.s], kb * 16, tl.row0 + i * TOK_BOX, 0);
+            }
+            sc.next();
+            ++s_issued;
+          }
+          if (!wait_bar(&empty[s], ph ^ 1u, &sm.abort, p.status)) {
             ok = false;
             break;
           }
-          uint64_t *bar = &sm.full[ring.s];
+          uint64_t *bar = &full[s];
           ptx::mbar_arrive_expect_tx(bar, tx);
-          ptx::tma_load_3d(stage_a + ring.s * C::A_BYTES, &tmA, bar, kb * ROW, tl.blk * BM, tl.e);
-          if (SF_TMA) ptx::tma_load_3d(stage_sa + ring.s * C::SA_BYTES, &tmSA, bar, kb * 16, tl.blk * BM, tl.e);
-          for (int i = 0; i < boxes; ++i) {
-            ptx::tma_load_3d(stage_b + ring.s * C::B_BYTES + i * TOK_BOX * ROW, &tmB, bar, kb * ROW,
-                             tl.row0 + i * TOK_BOX, 0);
-            if (SF_TMA)
-              ptx::tma_load_3d(stage_sb + ring.s * C::SB_BYTES + i * TOK_BOX * 16, &tmSB, bar, kb * 16,
-                               tl.row0 + i * TOK_BOX, 0);
+          if (weights) {
+            ptx::tma_load_3d(stage_a + s * C::A_BYTES, &tmA, bar, kb * ROW, tl.blk * BM, tl.e);
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              ptx::tma_load_3d(stage_b + s * C::B_BYTES + i * TOK_BOX * ROW, &tmB, bar, kb * ROW, tl.row0 + i * TOK_BOX,
+                               0);
+          }
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1u;
           }
         }
       }
-      for (int s = 0; s < STAGES; ++s) {
-        if ((uint32_t)s >= issued) break;
-        const uint32_t last = (issued - 1 - s) / STAGES;
-        drain_bar(&sm.full[s], last & 1u, p.status);
-      }
+      // every issued copy has landed before shared memory is released
+      for (int i = 0; i < stages && (uint32_t)i < issued; ++i)
+        drain_bar(&full[i], (issued - 1 - i) / stages & 1u, p.status);
+      for (int i = 0; i < S_STAGES && (uint32_t)i < s_issued; ++i)
+        drain_bar(&sm.s_full[i], (s_issued - 1 - i) / S_STAGES & 1u, p.status);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -242,9 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       const uint64_t ad0 = ptx::desc_kmajor_sw128(ptx::smem_addr(stage_a));
       const uint64_t bd0 = ptx::desc_kmajor_sw128(ptx::smem_addr(stage_b));
-      Ring<STAGES> ring;
+      Ring<C::A_STAGES> ra;
+      Ring<C::B_STAGES> rb;
       Ring<C::SF_BUFS> sf;
-      bool ready = false, sf_ready = false;  // the next stage's barriers, read ahead
+      bool a_ready = false, b_ready = false, sf_ready = false;  // the next stage's barriers, read ahead
       int i = 0;
       bool ok = true;
       for (int t = unit; t < total && ok; t += n_units, ++i) {
@@ -256,27 +292,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d_tmem = tmem_base + acc * BT;
         const uint32_t idesc = kIdesc0 | (uint32_t)((tl.count + 15) >> 4) << 18;  // N >> 3 at bit 17
         for (int kb = kb0; kb < kb1; ++kb) {
-          if ((!ready && !wait_bar(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) ||
+          if ((!a_ready && !wait_bar(&sm.a_full[ra.s], ra.ph, &sm.abort, p.status)) ||
+              (!b_ready && !wait_bar(&sm.b_full[rb.s], rb.ph, &sm.abort, p.status)) ||
               (!sf_ready && !wait_bar(&sm.sf_full[sf.s], sf.ph, &sm.abort, p.status))) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          Ring<STAGES> nx = ring;
-          nx.next();
+          const int as = ra.s, bs = rb.s;
+          ra.next();
+          rb.next();
           Ring<C::SF_BUFS> sn = sf;
           sn.next();
-          ready = ptx::mbar_try_wait(&sm.full[nx.s], nx.ph);
+          a_ready = ptx::mbar_try_wait(&sm.a_full[ra.s], ra.ph);
+          b_ready = ptx::mbar_try_wait(&sm.b_full[rb.s], rb.ph);
           sf_ready = ptx::mbar_try_wait(&sm.sf_full[sn.s], sn.ph);
-          const uint64_t ad = ad0 + (uint32_t)ring.s * (C::A_BYTES >> 4), bd = bd0 + (uint32_t)ring.s * (C::B_BYTES >> 4);
+          const uint64_t ad = ad0 + (uint32_t)as * (C::A_BYTES >> 4), bd = bd0 + (uint32_t)bs * (C::B_BYTES >> 4);
           const uint32_t sfa = tmem_base + C::SF_BASE + sf.s * C::SF_COLS, sfb = sfa + C::SFA_COLS;
 #pragma unroll
           for (int k = 0; k < STEPS; ++k)
             mma_nvfp4(d_tmem, ad + k * (MMA_K / 2 >> 4), bd + k * (MMA_K / 2 >> 4), idesc, sfa + k * (BM / 32),
                       sfb + k * (BT / 32), ((kb - kb0) | k) != 0);
-          ptx::mma_commit(&sm.empty[ring.s]);
+          ptx::mma_commit(&sm.a_empty[as]);
+          ptx::mma_commit(&sm.b_empty[bs]);
           ptx::mma_commit(&sm.sf_empty[sf.s]);
-          ring = nx;
           sf = sn;
         }
         if (ok) ptx::mma_commit(&sm.tmem_full[acc]);
@@ -285,13 +324,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_bar(&sm.drain, 0, p.status);
     }
     __syncwarp();
-  } else if (warp >= kScaleWarp0) {
+  } else if (warp >= kScaleWarp0 && warp < kTokenWarp) {
     // ================================================= scales to TMEM
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     constexpr int AR = BM / 32, BR = BT / 32;  // rows of each operand a lane
     const bool words = (p.K & 63) == 0;
     const int pitch = p.K / 16;
-    Ring<STAGES> ring;
+    Ring<S_STAGES> sc;
     Ring<C::SF_BUFS> sf;
     bool ok = true;
     for (int t = unit; t < total && ok; t += n_units) {
@@ -311,25 +350,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (!SF_TMA) fetch(kb0);
-      for (int kb = kb0; kb < kb1; ++kb, ring.next(), sf.next()) {
+      for (int kb = kb0; kb < kb1; ++kb, sf.next()) {
+        const int at_k = (kb - kb0) % SPAN;  // 16-byte piece of the scale rows
         if (SF_TMA) {
-          if (!warp_wait(&sm.full[ring.s], ring.ph, &sm.abort, p.status)) {
+          if (at_k == 0 && !warp_wait(&sm.s_full[sc.s], sc.ph, &sm.abort, p.status)) {
             ok = false;
             break;
           }
           __syncwarp();
-          const uint4 *a = reinterpret_cast<const uint4 *>(stage_sa + ring.s * C::SA_BYTES) + lane;
-          const uint4 *b = reinterpret_cast<const uint4 *>(stage_sb + ring.s * C::SB_BYTES) + lane;
+          // rows 64 bytes apart: 16-byte piece c of row r at c ^ (r / 2 % 4) (64-byte swizzle)
+          const uint4 *a = reinterpret_cast<const uint4 *>(stage_s + sc.s * C::S_BYTES) + lane * SPAN +
+                           (at_k ^ ((lane >> 1) & 3));
+          const uint4 *b = a + BM * SPAN;
 #pragma unroll
           for (int j = 0; j < AR; ++j) {
-            const uint4 v = a[j * 32];
+            const uint4 v = a[j * 32 * SPAN];
             va[j][0] = v.x, va[j][1] = v.y, va[j][2] = v.z, va[j][3] = v.w;
           }
 #pragma unroll
           for (int j = 0; j < BR; ++j) {
-            const uint4 v = b[j * 32];
+            const uint4 v = b[j * 32 * SPAN];
             vb[j][0] = v.x, vb[j][1] = v.y, vb[j][2] = v.z, vb[j][3] = v.w;
           }
+        }
+        if (SF_TMA && (at_k == SPAN - 1 || kb == kb1 - 1)) {  // the stage's last rows are in registers
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sm.s_empty[sc.s]);
+          sc.next();
         }
         if (!warp_wait(&sm.sf_empty[sf.s], sf.ph ^ 1u, &sm.abort, p.status)) {
           ok = false;
@@ -411,10 +458,10 @@ moe_status launch(Params &p, const void *a, const void *w, cudaStream_t s) {
     return MOE_ERR_CUDA;
   tsa = ta;
   tsb = tb;
-  if (SF_TMA && (!tma_map_u8(&tsa, p.sw, (uint64_t)p.K / 16, p.N, p.E, 16, BM) ||
-                 !tma_map_u8(&tsb, p.sa, (uint64_t)p.K / 16, p.rows, 1, 16, TOK_BOX)))
+  if (SF_TMA && (!tma_map_u8(&tsa, p.sw, (uint64_t)p.K / 16, p.N, p.E, SROW, BM, SROW) ||
+                 !tma_map_u8(&tsb, p.sa, (uint64_t)p.K / 16, p.rows, 1, SROW, TOK_BOX, SROW)))
     return MOE_ERR_CUDA;
-  const size_t smem = 1024 + (size_t)C::STAGES * C::STAGE_BYTES + kSmemPart + kRowStage;
+  const size_t smem = 1024 + (size_t)C::BYTES + kSmemPart + kRowStage;
   auto kern = grouped_gemm_fp4<BT, SF_TMA>;
   static std::atomic<uint64_t> known[kMaxDevices];
   Launch l;
