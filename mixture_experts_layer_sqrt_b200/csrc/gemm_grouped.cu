@@ -24,12 +24,12 @@
 // are set to zero in both operands before the MMAs read them, so that nothing
 // there, NaN included, reaches this group's sum.
 //
-// Roles (192 threads per CTA, 224 for TN; persistent, one CTA per SM):
+// Roles (320 threads per CTA, 224 for TN; persistent, one CTA per SM):
 //   warp 0    TMA producer into the stage ring
 //   warp 1    TMEM owner; one thread issues the MMAs (4 x K=16 per stage);
 //             two accumulators let the epilogue of tile i overlap the MMAs
 //             of tile i+1
-//   warps 2-5 epilogue: TMEM lane = output feature
+//   warps 2-9 epilogue: TMEM lane = output feature (TN: warps 2-5)
 //   warp 6    TN: clears the lines above and hands the stage on to the MMAs
 //
 // Every wait is bounded (2 s, then MOE_ERR_DEVICE_TIMEOUT in the status word
@@ -73,7 +73,9 @@ struct Cfg {
   static constexpr uint32_t TMEM_COLS = 2 * BT;
 };
 template <Mode MODE>
-constexpr int kThreads = MODE == TN ? 224 : 192;
+constexpr int kEpiWarps = MODE == TN ? 4 : 4 * kEpiGroups;
+template <Mode MODE>
+constexpr int kThreads = MODE == TN ? 224 : 320;
 constexpr int kClearWarp = 6;  // TN
 
 template <int STAGES>
@@ -85,13 +87,13 @@ struct Smem {
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint64_t drain;
-  __align__(16) float wbuf[4 * 32];  // row factors, 32 an epilogue warp
+  __align__(16) float wbuf[4 * kEpiGroups * 32];  // row factors, 32 an epilogue warp
   uint32_t tmem_base;
   int abort;
   int start[MAX_E + 1];
   int off[MAX_E + 1];
 };
-constexpr int kSmemPart = 9216;             // barriers and tile list
+constexpr int kSmemPart = 9728;             // barriers and tile list
 constexpr int kStaging = 4 * 32 * 32 * 4;   // epilogue: 4 KB a warp (TN), or two buffers of 32 tokens
 static_assert(kStaging == kRowStage, "one size for both epilogues");
 static_assert(sizeof(Smem<8>) <= kSmemPart, "the epilogue staging follows the barriers and tile list");
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&sm.tmem_full[a], 1);
-      ptx::mbar_init(&sm.tmem_empty[a], PAIR ? 8 : 4);  // epilogue warps
+      ptx::mbar_init(&sm.tmem_empty[a], (PAIR ? 2 : 1) * kEpiWarps<MODE>);
     }
     ptx::mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -422,8 +424,9 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       phase ^= 1u << s;
     }
   } else {
-    // ================================================= epilogue (warps 2..5)
-    const int q = warp & 3;  // TMEM lane quadrant this warp may access
+    // ================================================= epilogue (from warp 2 on)
+    const int q = warp & 3;              // TMEM lane quadrant this warp may access
+    const int group = (warp - 2) >> 2;   // NT, NN
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
     const RowStore store = {p.out, p.out_f32, p.N, p.row_weight, nullptr};
     int i = 0;
@@ -432,22 +435,23 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       const bool have = tl.red > 0;
       const int acc = i & 1;
       const uint32_t aph = (i >> 1) & 1u;
+      const float w0 = MODE != TN ? row_factor(store, tl.row0, tl.count, group * 32) : 1.0f;
       if (have) {
         ++i;
-        if (!epi_all(warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status))) break;
+        if (!all_agree<3, 32 * kEpiWarps<MODE>>(warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status))) break;
         ptx::tc_fence_after();
       }
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
       if (p.split > 1) {
         if (!have) {
         } else if (MODE != TN) {
-          put_part_columns(parts, tbase, tl.count, q);
+          put_part_columns(parts, tbase, tl.count, q, group, kEpiGroups);
         } else {
           put_part_features(parts, tbase, tl.count, p.tile + 4, q);
         }
       } else if (MODE != TN) {
-        store_tokens(store, tbase, tl.row0, tl.count, tl.m0 + (int)rank * BM, q, 1.0f,
-                     reinterpret_cast<uint8_t *>(staging), sm.wbuf + q * 32);
+        store_tokens<false>(store, tbase, tl.row0, tl.count, tl.m0 + (int)rank * BM, q, group, w0, 1.0f,
+                            reinterpret_cast<uint8_t *>(staging), sm.wbuf + (warp - 2) * 32);
       } else {
         // rows of dW, a lane each: 32 words of every row at a time through this
         // warp's 4 KB (16-byte piece j of row r at j ^ (r % 8)), so that every

@@ -20,13 +20,12 @@
 // 32-bit column per 32 rows (lane i of column j: the four scale bytes of row
 // 32 j + i), the same in all four lane quadrants.  Four warps, one a quadrant,
 // copy them there from the stage with tcgen05.st, one 16-byte read a row, up to
-// SF_BUFS stages ahead of the MMAs.  Scale rows that TMA cannot read
-// (K not a multiple of 256: rows not a multiple of 16 bytes) are loaded by the
-// same warps from global memory, one stage ahead in registers.
+// SF_BUFS stages ahead of the MMAs.  Scale rows that TMA cannot read (K not a
+// multiple of 256: rows not a multiple of 16 bytes) are copied by the same warps.
 //
-// Roles (352 threads, persistent, one CTA per SM): warp 0 TMA producer of the
-// weights, warp 1 TMEM owner and MMA issuer, warps 2-5 epilogue, warps 6-9
-// scales, warp 10 TMA producer of the tokens.  Every wait is bounded.
+// Roles (480 threads, persistent, one CTA per SM): warp 0 TMA producer of the
+// weights, warp 1 TMEM owner and MMA issuer, warps 2-9 epilogue, warps 10-13
+// scales, warp 14 TMA producer of the tokens.  Every wait is bounded.
 #include <cudaTypedefs.h>
 #include <limits.h>
 
@@ -51,18 +50,25 @@ constexpr int TOK_BOX = 32;             // token rows per TMA box
 constexpr int SPAN = 4;                 // stages of codes that a stage of scales covers
 constexpr int SROW = 16 * SPAN;         // its bytes a row
 constexpr int S_STAGES = 2;
-constexpr int kThreads = 352;
-constexpr int kScaleWarp0 = 6;
-constexpr int kTokenWarp = 10;
+constexpr int kRawSpan = 2;             // and of raw scale rows, the path without TMA
+constexpr int kRawRow = 16 * (kRawSpan + 1);
+constexpr int kThreads = 480;
+constexpr int kScaleWarp0 = 10;
+constexpr int kTokenWarp = 14;
 
-template <int BT>
+template <int BT, bool SF_TMA>
 struct Cfg {
   static constexpr int A_BYTES = BM * ROW, B_BYTES = BT * ROW;  // codes of a stage
   // Rings of their own: the weights come from DRAM, the tokens mostly from L2.
-  static constexpr int A_STAGES = BT == 192 ? 4 : 8;
+  static constexpr int A_STAGES = (BT == 192 ? 4 : 8) - (SF_TMA ? 0 : 1);
   static constexpr int B_STAGES = BT == 192 ? 4 : 5;
   static constexpr int S_BYTES = (BM + BT) * SROW;              // scales of SPAN stages
-  static constexpr int BYTES = A_STAGES * A_BYTES + B_STAGES * B_BYTES + S_STAGES * S_BYTES;
+  // without TMA: stages of raw scale rows, in the space of these and of a weight stage
+  static constexpr int RAW_STAGES = 3;
+  static constexpr int RAW_BYTES = (BM + BT) * kRawRow;
+  static constexpr int ROWS_BYTES = (BM + BT) * 16 * kRawSpan;  // one of them in place
+  static constexpr int BYTES =
+      A_STAGES * A_BYTES + B_STAGES * B_BYTES + (SF_TMA ? S_STAGES * S_BYTES : RAW_STAGES * RAW_BYTES + ROWS_BYTES);
   static constexpr int SFA_COLS = STEPS * BM / 32;   // TMEM columns of a stage's scales
   static constexpr int SFB_COLS = STEPS * BT / 32;
   static constexpr int SF_COLS = SFA_COLS + SFB_COLS;
@@ -81,13 +87,13 @@ struct Smem {
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint64_t drain;
-  __align__(16) float wbuf[4 * 32];  // row factors, 32 an epilogue warp
+  __align__(16) float wbuf[4 * kEpiGroups * 32];  // row factors, 32 an epilogue warp
   uint32_t tmem_base;
   int abort;
   int start[MAX_E + 1];
   int off[MAX_E + 1];
 };
-constexpr int kSmemPart = 9216;
+constexpr int kSmemPart = 9728;
 static_assert(sizeof(Smem) <= kSmemPart, "barriers and tile list");
 
 struct Params {
@@ -127,16 +133,32 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // [27,29), scale data ids 0, K = 64 (bit 31 = 0).
 constexpr uint32_t kIdesc0 = (1u << 7) | (1u << 10) | ((uint32_t)(BM >> 7) << 27);
 
-// Up to 16 scale bytes of a row, `left` of them present (a multiple of 2).
-__device__ __forceinline__ void load_scales(const uint8_t *p, int left, bool words, uint32_t (&w)[4]) {
+// Scale rows that TMA cannot read start at any even byte.  The scale warps copy
+// the aligned 16-byte chunks that hold a row's next kRawSpan stages (three) as
+// they are, asynchronously, two such runs ahead, and then shift them into place, a
+// row a thread.  (Loads into registers instead of the copies took 155 us for 8262
+// rows x 2080 x 2040 over 67 groups, a shift by every warp that reads them 128.)
+// 16 bytes to shared memory, the first `bytes` of them read and the others zero.
+__device__ __forceinline__ void copy_chunk(void *dst, const uint8_t *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_addr(dst)), "l"(src), "r"(bytes)
+               : "memory");
+}
+// 16 bytes from byte `shift` (even, < 16) of two chunks on, those from `left` on zero.
+__device__ __forceinline__ void shifted(const uint8_t *chunks, int shift, int left, uint32_t (&v)[4]) {
+  const uint4 lo = reinterpret_cast<const uint4 *>(chunks)[0], hi = reinterpret_cast<const uint4 *>(chunks)[1];
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t u[6], t[5];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    w[k] = 0;
-    if (words) {  // rows a multiple of 4 bytes
-      if (4 * k < left) w[k] = __ldg(reinterpret_cast<const uint32_t *>(p) + k);
-    } else {
-      if (4 * k < left) w[k] = __ldg(reinterpret_cast<const uint16_t *>(p) + 2 * k);
-      if (4 * k + 2 < left) w[k] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(p) + 2 * k + 1) << 16;
+  for (int i = 0; i < 6; ++i) u[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) t[i] = shift & 4 ? u[i + 1] : u[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(t[i], t[i + 1], (shift & 2) * 8);
+  if (left < 16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * i + 2 >= left) v[i] &= 0xFFFFu;
+      if (4 * i >= left) v[i] = 0;
     }
   }
 }
@@ -146,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_fp4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                      const Params p) {
-  using C = Cfg<BT>;
+  using C = Cfg<BT, SF_TMA>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *stage_a = base;
@@ -177,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&sm.tmem_full[a], 1);
-      ptx::mbar_init(&sm.tmem_empty[a], 4);
+      ptx::mbar_init(&sm.tmem_empty[a], 4 * kEpiGroups);
     }
     ptx::mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -328,33 +350,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================================================= scales to TMEM
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     constexpr int AR = BM / 32, BR = BT / 32;  // rows of each operand a lane
-    const bool words = (p.K & 63) == 0;
-    const int pitch = p.K / 16;
     Ring<S_STAGES> sc;
     Ring<C::SF_BUFS> sf;
     bool ok = true;
-    for (int t = unit; t < total && ok; t += n_units) {
+    // the path without TMA
+    const int pitch = p.K / 16, tid = threadIdx.x - kScaleWarp0 * 32;
+    int raw = 0;  // stage of raw rows to read
+    uint8_t *const in_place = stage_s + C::RAW_STAGES * C::RAW_BYTES;
+    // the copies run RAW_STAGES - 1 stages ahead, over the tiles' ends
+    int c_t = unit, c_kb = kb0, c_stage = 0;
+    TokenTile c_tl = {};
+    if (!SF_TMA && unit < total) c_tl = tile_of(unit);
+    auto copy = [&]() {
+      if (c_t < total) {
+        // offsets from the tile's first rows, rounded down to a chunk
+        const long wt = ((long)c_tl.e * p.N + c_tl.blk * BM) * pitch + c_kb * 16, tk = (long)c_tl.row0 * pitch + c_kb * 16;
+        const int left = min(pitch - c_kb * 16, 16 * kRawSpan);
+        const uint8_t *const w_at = p.sw + (wt & ~15l), *const t_at = p.sa + (tk & ~15l);
+        const int w_mis = (int)(wt & 15), t_mis = (int)(tk & 15);
+        const int w_all = (int)min((long)p.E * p.N * pitch - (wt & ~15l), 0x40000000l);
+        const int t_all = (int)min((long)p.rows * pitch - (tk & ~15l), 0x40000000l);
+        const int w_rows = min(p.N - c_tl.blk * BM, BM), t_rows = c_tl.count;
+        uint8_t *const dst = stage_s + c_stage * C::RAW_BYTES;
+#pragma unroll 4
+        for (int i = tid; i < (BM + BT) * (kRawSpan + 1); i += 128) {
+          const int row = i / (kRawSpan + 1), c = i - row * (kRawSpan + 1);
+          const bool weight = row < BM;
+          const int r = weight ? row : row - BM;
+          const int off = r * pitch + (weight ? w_mis : t_mis);
+          const int at = (off & ~15) + 16 * c;
+          const bool in = r < (weight ? w_rows : t_rows) && 16 * c < (off & 15) + left;
+          copy_chunk(dst + i * 16, (weight ? w_at : t_at) + (in ? at : 0), in ? min(16, (weight ? w_all : t_all) - at) : 0);
+        }
+        c_kb += kRawSpan;
+        if (c_kb >= kb1) {
+          c_kb = kb0;
+          c_t += n_units;
+          if (c_t < total) c_tl = tile_of(c_t);
+        }
+        c_stage = c_stage + 1 == C::RAW_STAGES ? 0 : c_stage + 1;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (!SF_TMA)
+      for (int i = 0; i < C::RAW_STAGES - 1; ++i) copy();
+    bool leave = false;
+    for (int t = unit; t < total && !leave; t += n_units) {
       const TokenTile tl = tile_of(t);
       uint32_t va[AR][4], vb[BR][4];
-      auto fetch = [&](int kb) {  // the path without TMA
-        const int left = pitch - kb * 16;
-#pragma unroll
-        for (int j = 0; j < AR; ++j) {
-          const int n = tl.blk * BM + j * 32 + lane;
-          load_scales(p.sw + ((long)tl.e * p.N + n) * pitch + kb * 16, n < p.N ? left : 0, words, va[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < BR; ++j) {
-          const int r = j * 32 + lane;
-          load_scales(p.sa + (long)(tl.row0 + r) * pitch + kb * 16, r < tl.count ? left : 0, words, vb[j]);
-        }
-      };
-      if (!SF_TMA) fetch(kb0);
+      const int a_mis = (int)(((long)tl.e * p.N + tl.blk * BM) * pitch & 15);  // of the tile's first rows
+      const int b_mis = (int)((long)tl.row0 * pitch & 15);
       for (int kb = kb0; kb < kb1; ++kb, sf.next()) {
-        const int at_k = (kb - kb0) % SPAN;  // 16-byte piece of the scale rows
         if (SF_TMA) {
+          const int at_k = (kb - kb0) % SPAN;  // 16-byte piece of the scale rows
           if (at_k == 0 && !warp_wait(&sm.s_full[sc.s], sc.ph, &sm.abort, p.status)) {
             ok = false;
+            leave = true;
             break;
           }
           __syncwarp();
@@ -372,15 +423,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint4 v = b[j * 32 * SPAN];
             vb[j][0] = v.x, vb[j][1] = v.y, vb[j][2] = v.z, vb[j][3] = v.w;
           }
+          if (at_k == SPAN - 1 || kb == kb1 - 1) {  // the stage's last rows are in registers
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sm.s_empty[sc.s]);
+            sc.next();
+          }
+        } else {
+          const int at_k = (kb - kb0) % kRawSpan;
+          if (at_k == 0) {
+            // the stage has landed for all, and the one before is read by all
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::RAW_STAGES - 2) : "memory");
+            ok = all_agree<4, 128>(ok);
+            if (!ok) {
+              leave = true;
+              break;
+            }
+            copy();
+            // into place, a row a thread: 16-byte piece c of row r at c ^ (r / 4 % 2)
+            const uint8_t *from = stage_s + raw * C::RAW_BYTES;
+            raw = raw + 1 == C::RAW_STAGES ? 0 : raw + 1;
+            const int left = pitch - kb * 16;
+            for (int r = tid; r < BM + BT; r += 128) {
+              const int shift = (r < BM ? a_mis + r * pitch : b_mis + (r - BM) * pitch) & 15;
+#pragma unroll
+              for (int c = 0; c < kRawSpan; ++c) {
+                uint32_t v[4];
+                shifted(from + r * kRawRow + c * 16, shift, left - c * 16, v);
+                *reinterpret_cast<uint4 *>(in_place + r * 16 * kRawSpan + ((c ^ ((r >> 2) & 1)) << 4)) =
+                    make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            }
+            asm volatile("bar.sync 5, 128;" ::: "memory");
+          }
+          const uint4 *a = reinterpret_cast<const uint4 *>(in_place) + lane * kRawSpan + (at_k ^ ((lane >> 2) & 1));
+          const uint4 *b = a + BM * kRawSpan;
+#pragma unroll
+          for (int j = 0; j < AR; ++j) {
+            const uint4 v = a[j * 32 * kRawSpan];
+            va[j][0] = v.x, va[j][1] = v.y, va[j][2] = v.z, va[j][3] = v.w;
+          }
+#pragma unroll
+          for (int j = 0; j < BR; ++j) {
+            const uint4 v = b[j * 32 * kRawSpan];
+            vb[j][0] = v.x, vb[j][1] = v.y, vb[j][2] = v.z, vb[j][3] = v.w;
+          }
         }
-        if (SF_TMA && (at_k == SPAN - 1 || kb == kb1 - 1)) {  // the stage's last rows are in registers
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sm.s_empty[sc.s]);
-          sc.next();
-        }
-        if (!warp_wait(&sm.sf_empty[sf.s], sf.ph ^ 1u, &sm.abort, p.status)) {
-          ok = false;
-          break;
+        ok = ok && warp_wait(&sm.sf_empty[sf.s], sf.ph ^ 1u, &sm.abort, p.status);
+        if (!ok) {
+          leave = SF_TMA;
+          if (SF_TMA) break;
+          continue;  // without TMA the warps leave together, at the next raw stage
         }
         ptx::tc_fence_after();
         uint32_t ca[C::SFA_COLS], cb[C::SFB_COLS];
@@ -396,7 +488,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < C::SFA_COLS; c += 8) tmem_st8(at + c, ca + c);
 #pragma unroll
         for (int c = 0; c < C::SFB_COLS; c += 8) tmem_st8(at + C::SFA_COLS + c, cb + c);
-        if (!SF_TMA && kb + 1 < kb1) fetch(kb + 1);
         tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
@@ -404,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ================================================= epilogue (warps 2..5)
-    const int q = warp & 3;
+    // ================================================= epilogue (warps 2..9)
+    const int q = warp & 3, group = (warp - 2) >> 2;
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
     const RowStore store = {p.out, p.out_f32, p.N, p.ra, p.row_weight};
     int i = 0;
@@ -414,12 +505,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int acc = i & 1;
       const uint32_t aph = (i >> 1) & 1u;
       const int n = tl.blk * BM + q * 32 + lane;
+      const float w0 = row_factor(store, tl.row0, tl.count, group * 32);
       const float wn = p.rw && n < p.N ? p.rw[(long)tl.e * p.N + n] : 1.0f;
-      if (!epi_all(warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status))) break;
+      if (!all_agree<3, 128 * kEpiGroups>(warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status))) break;
       ptx::tc_fence_after();
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
-      if (p.split > 1) put_part_columns(parts, tbase, tl.count, q);
-      else store_tokens(store, tbase, tl.row0, tl.count, tl.blk * BM, q, wn, staging, sm.wbuf + q * 32);
+      if (p.split > 1) put_part_columns(parts, tbase, tl.count, q, group, kEpiGroups);
+      else store_tokens<true>(store, tbase, tl.row0, tl.count, tl.blk * BM, q, group, w0, wn, staging,
+                              sm.wbuf + (warp - 2) * 32);
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.tmem_empty[acc]);
@@ -451,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int BT, bool SF_TMA>
 moe_status launch(Params &p, const void *a, const void *w, cudaStream_t s) {
-  using C = Cfg<BT>;
+  using C = Cfg<BT, SF_TMA>;
   CUtensorMap ta, tb, tsa, tsb;
   if (!tma_map_u8(&ta, w, (uint64_t)p.K / 2, p.N, p.E, ROW, BM, 128) ||
       !tma_map_u8(&tb, a, (uint64_t)p.K / 2, p.rows, 1, ROW, TOK_BOX, 128))
@@ -520,6 +613,7 @@ moe_status launch_grouped_nvfp4(const MoEGrouped &g, const void *a, const void *
   p.status = status;
   const bool narrow = g.rows <= 64l * g.groups;  // as in gemm_grouped.cu
   const bool sf_tma = g.k % 256 == 0;
+  if (!sf_tma && g.k > 1 << 26) return MOE_ERR_UNSUPPORTED;  // a tile's scale offsets in 32 bits
   if (narrow) return sf_tma ? launch<64, true>(p, a, w, s) : launch<64, false>(p, a, w, s);
   return sf_tma ? launch<192, true>(p, a, w, s) : launch<192, false>(p, a, w, s);
 }

@@ -205,29 +205,35 @@ __device__ __forceinline__ TokenTile token_tile(const int *start, const int *off
 }
 
 // ---------------------------------------------------------------- epilogue
-// Four warps store a tile of 128 output features (TMEM lanes) x `count` tokens
-// (columns) to rows of y [rows, N].
+// Eight warps store a tile of 128 output features (TMEM lanes) x `count` tokens
+// (columns) to rows of y [rows, N]: two groups of four, a warp a lane quadrant,
+// that take turns at 32 tokens.  (One group took 925 cycles per 32 tokens, the
+// dependent latencies of one warp a scheduler; a tile of 256 tokens with a short
+// reduction, K = 96, was bound by that.)
 //
-// bf16: a lane holds one feature of 32 tokens.  Lanes exchange halves so that
-// each holds pairs of features, the four warps put 32 tokens x 128 features
-// into shared memory (256 bytes a token; the 64-byte quarter of warp q of token
-// t at q ^ (t & 1), so that the two tokens of a store take all banks), and each
-// warp writes whole 256-byte rows of 8 tokens.  Two buffers, one barrier a
-// round.  fp32: a warp's store is 128 bytes of a row as it is.
-constexpr int kRowStage = 2 * 32 * 256;  // bytes
-constexpr int kEpiBarrier = 1;           // named barrier of the 128 epilogue threads
-
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync %0, 128;" ::"n"(kEpiBarrier) : "memory"); }
-// The same decision for all epilogue warps: true if `ok` is in every thread.
-__device__ __forceinline__ bool epi_all(bool ok) {
+// bf16: a lane holds one feature of 32 tokens.  It packs two tokens at a time
+// and trades with its neighbour, after which the even lane holds features (n,
+// n + 1) of the first and the odd lane (n - 1, n) of the second; the four warps
+// put 32 tokens x 128 features into shared memory (256 bytes a token; the
+// 64-byte quarter of warp q of token t at q ^ (t & 1), so that the two tokens of
+// a store take all banks), and each warp writes whole 256-byte rows of 8 tokens.
+// fp32: a warp's store is 128 bytes of a row as it is.
+constexpr int kRowStage = 2 * 32 * 256;  // bytes: a buffer a group
+constexpr int kEpiGroups = 2;
+// Named barriers of the epilogue: 1 and 2 for the groups, 3 for all its warps, 4
+// for the scale warps of gemm_grouped_fp4.cu.
+__device__ __forceinline__ void epi_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+// The same decision for all `threads` of the barrier: true if `ok` is in every one.
+template <int BARRIER, int THREADS>
+__device__ __forceinline__ bool all_agree(bool ok) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}\n"
       : "=r"(r)
-      : "r"((uint32_t)ok), "n"(kEpiBarrier)
+      : "r"((uint32_t)ok), "n"(BARRIER), "n"(THREADS)
       : "memory");
   return r != 0;
 }
@@ -248,10 +254,11 @@ struct RowStore {
 //   by feature [feature][column], pitch columns + 4: rows of dW
 constexpr int kColPitch = 132;
 
-__device__ __forceinline__ void put_part_columns(float *parts, uint32_t tbase, int count, int q) {
+// Warps of group `group` of `groups` take every groups-th run of 32 columns.
+__device__ __forceinline__ void put_part_columns(float *parts, uint32_t tbase, int count, int q, int group, int groups) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int c = 0; c < count; c += 32) {
+  for (int c = group * 32; c < count; c += groups * 32) {
     uint32_t v[32];
     ptx::tmem_ld32(tbase + c, v);
     ptx::tmem_ld_wait();
@@ -350,42 +357,55 @@ __device__ __forceinline__ void store_summed_tokens(const RowStore &o, const flo
   }
 }
 
-// q: this warp's lane quadrant; n0: the tile's first feature; scale: this
-// lane's feature factor.  stage: kRowStage bytes shared by the four warps;
-// wbuf: 32 floats of this warp's.
+// The factor of a tile's token c + lane.  Read a round ahead of its use (the
+// first before the wait for the tile): its latency, a round after the other,
+// made a short reduction's epilogue five times as long.
+__device__ __forceinline__ float row_factor(const RowStore &o, int row0, int count, int c) {
+  const int t = c + (threadIdx.x & 31);
+  float w = 1.0f;
+  if (t < count) {
+    if (o.w0) w = o.w0[row0 + t];
+    if (o.w1) w *= o.w1[row0 + t];
+  }
+  return w;
+}
+
+// q: this warp's lane quadrant; n0: the tile's first feature; w: row_factor of
+// the group's first round; SCALED: times `scale`, this lane's feature factor.
+// stage: kRowStage bytes; wbuf: 32 floats of this warp's.
+template <bool SCALED>
 __device__ __forceinline__ void store_tokens(const RowStore &o, uint32_t tbase, int row0, int count, int n0, int q,
-                                             float scale, uint8_t *stage, float *wbuf) {
+                                             int group, float w, float scale, uint8_t *stage, float *wbuf) {
   const int lane = threadIdx.x & 31;
   const int n = n0 + q * 32 + lane;
   const bool weighted = o.w0 || o.w1;
   const int odd = lane & 1;
+  constexpr int step = 32 * kEpiGroups;
+  if (group * 32 >= count) return;  // all four warps of the group
+  uint8_t *buf = stage + group * (kRowStage / kEpiGroups);
   uint32_t v[32];
-  ptx::tmem_ld32(tbase, v);
+  ptx::tmem_ld32(tbase + group * 32, v);
 #pragma unroll 1
-  for (int c = 0; c < count; c += 32) {
+  for (int c = group * 32; c < count; c += step) {
     const int left = count - c;
     if (weighted) {
-      float w = 1.0f;
-      if (lane < left) {
-        if (o.w0) w = o.w0[row0 + c + lane];
-        if (o.w1) w *= o.w1[row0 + c + lane];
-      }
       __syncwarp();
       wbuf[lane] = w;
       __syncwarp();
+      if (c + step < count) w = row_factor(o, row0, count, c + step);
     }
     ptx::tmem_ld_wait();
     float f[32];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]) * scale;
+    for (int j = 0; j < 32; ++j) f[j] = SCALED ? __uint_as_float(v[j]) * scale : __uint_as_float(v[j]);
     if (weighted) {
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
-        const float4 w = *reinterpret_cast<const float4 *>(wbuf + j);
-        f[j] *= w.x, f[j + 1] *= w.y, f[j + 2] *= w.z, f[j + 3] *= w.w;
+        const float4 k = *reinterpret_cast<const float4 *>(wbuf + j);
+        f[j] *= k.x, f[j + 1] *= k.y, f[j + 2] *= k.z, f[j + 3] *= k.w;
       }
     }
-    if (c + 32 < count) ptx::tmem_ld32(tbase + c + 32, v);
+    if (c + step < count) ptx::tmem_ld32(tbase + c + step, v);
     if (o.out_f32) {
       float *y = (float *)o.out + (long)(row0 + c) * o.N + n;
       if (n < o.N) {
@@ -395,29 +415,32 @@ __device__ __forceinline__ void store_tokens(const RowStore &o, uint32_t tbase, 
       }
       continue;
     }
-    uint8_t *buf = stage + ((c >> 5) & 1) * (kRowStage / 2);
+    if (c != group * 32) epi_sync(group);  // the round before has been read
+    uint8_t *at = buf + odd * 256 + ((q ^ odd) << 6) + ((lane & ~1) << 1);
+    const uint32_t pick = odd ? 0x3276u : 0x5410u;  // odd: (other's high, own high), even: (own low, other's low)
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
-      // the even lane keeps token j, features (n, n + 1); the odd one token j + 1, (n - 1, n)
-      const float other = __shfl_xor_sync(0xffffffffu, odd ? f[j] : f[j + 1], 1);
-      const __nv_bfloat162 p = odd ? __floats2bfloat162_rn(other, f[j + 1]) : __floats2bfloat162_rn(f[j], other);
-      *reinterpret_cast<__nv_bfloat162 *>(buf + (j + odd) * 256 + ((q ^ odd) << 6) + ((lane & ~1) << 1)) = p;
+      const __nv_bfloat162 p = __floats2bfloat162_rn(f[j], f[j + 1]);
+      const uint32_t own = *reinterpret_cast<const uint32_t *>(&p);
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+      *reinterpret_cast<uint32_t *>(at + j * 256) = __byte_perm(own, other, pick);
     }
-    epi_sync();
+    epi_sync(group);
     // this warp's 8 tokens, two a round: 16 lanes x 16 bytes each
     const int piece = lane & 15, half = lane >> 4;
     const bool in = n0 + piece * 8 < o.N;
-    uint4 w[4];
+    uint4 rows[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = q * 8 + 2 * i + half;
-      w[i] = *reinterpret_cast<const uint4 *>(buf + t * 256 + (((piece >> 2) ^ (t & 1)) << 6) + ((piece & 3) << 4));
+      rows[i] = *reinterpret_cast<const uint4 *>(buf + t * 256 + (((piece >> 2) ^ (t & 1)) << 6) + ((piece & 3) << 4));
     }
     __nv_bfloat16 *y = (__nv_bfloat16 *)o.out + (long)(row0 + c + q * 8 + half) * o.N + n0 + piece * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (in && q * 8 + 2 * i + half < left) *reinterpret_cast<uint4 *>(y + (long)(2 * i) * o.N) = w[i];
+      if (in && q * 8 + 2 * i + half < left) *reinterpret_cast<uint4 *>(y + (long)(2 * i) * o.N) = rows[i];
   }
+  if (!o.out_f32) epi_sync(group);  // read before the next tile's first round
 }
 
 }  // namespace grouped
