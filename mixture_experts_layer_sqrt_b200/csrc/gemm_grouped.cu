@@ -82,7 +82,6 @@ template <int STAGES>
 struct Smem {
   uint64_t full[STAGES];    // stage ready for the MMAs
   uint64_t landed[STAGES];  // TN: the copies of a last, partial block are complete in this CTA
-  uint64_t cleared[STAGES]; // TN, leader: and the peer has cleared its lines
   uint64_t empty[STAGES];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
@@ -111,6 +110,15 @@ struct Params {
   int accumulate;  // TN
   int *status;
 };
+
+// Both arrivals of a barrier that counts two, and the bytes to expect.
+__device__ __forceinline__ void arrive2_expect_tx(uint64_t *bar, uint32_t bytes) {
+  asm volatile(
+      "mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n\t"
+      "mbarrier.arrive.shared::cta.b64 _, [%0], 2;" ::"r"(ptx::smem_addr(bar)),
+      "r"(bytes)
+      : "memory");
+}
 
 __device__ __forceinline__ void spin_ns(uint64_t ns) {
   const uint64_t t0 = ptx::globaltimer_ns();
@@ -160,8 +168,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      ptx::mbar_init(&sm.full[s], 1);
-      ptx::mbar_init(&sm.cleared[s], 1);
+      ptx::mbar_init(&sm.full[s], MODE == TN ? 2 : 1);  // TN: a partial block is handed on by both CTAs
       ptx::mbar_init(&sm.landed[s], 1);
       ptx::mbar_init(&sm.empty[s], 1);
     }
@@ -277,7 +284,10 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
           if (PAIR && !partial) {
             // both CTAs' copies complete on the leader's barrier
             const uint32_t lead_bar = ptx::map_to_rank(bar, lead);
-            if (rank == 0) ptx::mbar_arrive_expect_tx(bar, 2 * tx);
+            if (rank == 0) {
+              if (MODE == TN) arrive2_expect_tx(bar, 2 * tx);
+              else ptx::mbar_arrive_expect_tx(bar, 2 * tx);
+            }
             if (MODE == NT) {
               ptx::tma_load_3d_pair(a, &tmA, lead_bar, k0, m0, tl.e);
             } else if (MODE == NN) {
@@ -405,21 +415,20 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       if (!warp_wait(&sm.landed[s], phase >> s & 1, &sm.abort, p.status)) break;
       __syncwarp();
       // lines [left, the MMAs' last) of every box
-      uint8_t *a = stage_a + s * A_BYTES, *b = stage_b + s * C::B_BYTES;
+      uint8_t *a = stage_a + s * A_BYTES + left * 128, *b = stage_b + s * C::B_BYTES + left * 128;
       const int boxes = (tl.staged() + 63) / 64;
       const int pieces = (((left + UMMA_K - 1) & ~(UMMA_K - 1)) - left) * 8;  // of 16 bytes, a box
-      for (int j = lane; j < pieces * (2 + boxes); j += 32) {
-        const int box = j / pieces, in = j - box * pieces;
-        uint8_t *q = (box < 2 ? a + box * BOX : b + (box - 2) * BOX) + left * 128 + in * 16;
-        *reinterpret_cast<uint4 *>(q) = make_uint4(0, 0, 0, 0);
+      for (int j = lane; j < pieces; j += 32) {
+#pragma unroll
+        for (int i = 0; i < 2 + C::B_ROWS / 64; ++i)
+          if (i < 2 + boxes)
+            *reinterpret_cast<uint4 *>((i < 2 ? a + i * BOX : b + (i - 2) * BOX) + j * 16) = make_uint4(0, 0, 0, 0);
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (rank != 0) {
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(&sm.cleared[s], lead));
-      } else {
-        if (!warp_wait(&sm.cleared[s], phase >> s & 1, &sm.abort, p.status)) break;
-        if (lane == 0) ptx::mbar_arrive(&sm.full[s]);
+      if (lane == 0) {
+        if (rank != 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(&sm.full[s], lead));
+        else ptx::mbar_arrive(&sm.full[s]);
       }
       phase ^= 1u << s;
     }
