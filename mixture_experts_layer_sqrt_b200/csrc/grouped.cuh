@@ -220,8 +220,8 @@ __device__ __forceinline__ TokenTile token_tile(const int *start, const int *off
 // fp32: a warp's store is 128 bytes of a row as it is.
 constexpr int kRowStage = 2 * 32 * 256;  // bytes: a buffer a group
 constexpr int kEpiGroups = 2;
-// Named barriers of the epilogue: 1 and 2 for the groups, 3 for all its warps, 4
-// for the scale warps of gemm_grouped_fp4.cu.
+// Named barriers of the epilogue: 1 and 2 for the groups, 3 for all its warps; 4
+// and 5 for the scale warps of gemm_grouped_fp4.cu.
 __device__ __forceinline__ void epi_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
 // The same decision for all `threads` of the barrier: true if `ok` is in every one.
 template <int BARRIER, int THREADS>

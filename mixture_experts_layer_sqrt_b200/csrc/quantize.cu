@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(32 * kWarps<SPAN>)
     if (!SWIGLU && row_token) {
       at = row_token[r];
       if (at < 0 || at >= src_rows) {  // never read: the row stays as it is
-        if (kChecked && lane == 0) note_violation();
+        if (kChecked && lane == 0 && part == 0) note_violation();
         continue;
       }
     }
