@@ -408,11 +408,11 @@ def grouped_matmul(a: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Ten
         with _on(d, stream):
             return grouped_matmul(a, w, offsets, transposed, row_weight, y, out, ws)
     if y is None:
-        y = a.new_empty((rows, N), dtype=odt)
+        y = a.new_empty(rows, N, dtype=odt)
     if ws is None:
         ws = workspace(256, a.device)
-    _check(lib.moe_grouped_matmul(g, _p(a), _p(offsets), _p(w), transposed, _p(row_weight), _p(y), _p(ws), ws.numel(),
-                                  _raw_stream(d)), "moe_grouped_matmul")
+    _check(lib.moe_grouped_matmul(g, a.data_ptr(), _p(offsets), w.data_ptr(), transposed, _p(row_weight), y.data_ptr(),
+                                  ws.data_ptr(), ws.numel(), _raw_stream(d)), "moe_grouped_matmul")
     return y
 
 
@@ -439,11 +439,11 @@ def grouped_wgrad(dy: torch.Tensor, a: torch.Tensor, offsets: Optional[torch.Ten
         with _on(d, stream):
             return grouped_wgrad(dy, a, offsets, dw, accumulate, out, ws)
     if dw is None:
-        dw = a.new_empty((E, N, K), dtype=odt)
+        dw = a.new_empty(E, N, K, dtype=odt)
     if ws is None:
         ws = workspace(256, a.device)
-    _check(lib.moe_grouped_wgrad(g, _p(dy), _p(a), _p(offsets), accumulate, _p(dw), _p(ws), ws.numel(),
-                                 _raw_stream(d)), "moe_grouped_wgrad")
+    _check(lib.moe_grouped_wgrad(g, dy.data_ptr(), a.data_ptr(), _p(offsets), accumulate, dw.data_ptr(),
+                                 ws.data_ptr(), ws.numel(), _raw_stream(d)), "moe_grouped_wgrad")
     return dw
 
 
@@ -473,11 +473,12 @@ def grouped_matmul_nvfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
             return grouped_matmul_nvfp4(a, a_scales, w, w_scales, offsets, a_row_scale, w_row_scale, row_weight, y, out,
                                         ws)
     if y is None:
-        y = a.new_empty((rows, N), dtype=odt)
+        y = a.new_empty(rows, N, dtype=odt)
     if ws is None:
         ws = workspace(256, a.device)
-    _check(lib.moe_grouped_matmul_nvfp4(g, _p(a), _p(a_scales), _p(a_row_scale), _p(offsets), _p(w), _p(w_scales),
-                                        _p(w_row_scale), _p(row_weight), _p(y), _p(ws), ws.numel(), _raw_stream(d)),
+    _check(lib.moe_grouped_matmul_nvfp4(g, a.data_ptr(), a_scales.data_ptr(), _p(a_row_scale), _p(offsets),
+                                        w.data_ptr(), w_scales.data_ptr(), _p(w_row_scale), _p(row_weight),
+                                        y.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(d)),
            "moe_grouped_matmul_nvfp4")
     return y
 
@@ -491,13 +492,14 @@ def _live(offsets: Optional[torch.Tensor]):
     return offsets.data_ptr() + 4 * (offsets.numel() - 1)
 
 
-def _nvfp4_outputs(rows: int, cols: int, x: torch.Tensor, row_scaled: bool, values: bool, out) -> Dict[str, torch.Tensor]:
+def _nvfp4_outputs(rows: int, cols: int, x: torch.Tensor, row_scaled: bool, values: bool,
+                   out) -> Dict[str, Optional[torch.Tensor]]:
     if out is None:
         u8 = torch.uint8
-        return dict(codes=x.new_empty((rows, cols // 2), dtype=u8),
-                    scales=x.new_empty((rows, cols // 16), dtype=u8),
-                    row_scale=x.new_empty((rows,), dtype=torch.float32) if row_scaled else None,
-                    values=x.new_empty((rows, cols), dtype=torch.bfloat16) if values else None)
+        return dict(codes=x.new_empty(rows, cols // 2, dtype=u8),
+                    scales=x.new_empty(rows, cols // 16, dtype=u8),
+                    row_scale=x.new_empty(rows, dtype=torch.float32) if row_scaled else None,
+                    values=x.new_empty(rows, cols, dtype=torch.bfloat16) if values else None)
     if (out.get("row_scale") is not None and not row_scaled) or (out.get("values") is not None and not values):
         raise ValueError("out has a tensor that this call does not write")
     _need(out.get("codes"), (rows, cols // 2), torch.uint8, "codes")
@@ -528,9 +530,9 @@ def quantize_nvfp4(x: torch.Tensor, row_token: Optional[torch.Tensor] = None, of
         with _on(d, stream):
             return quantize_nvfp4(x, row_token, offsets, row_scaled, values, out)
     o = _nvfp4_outputs(rows, cols, x, row_scaled, values, out)
-    _check(lib.moe_quantize_nvfp4(rows, cols, dt, _p(x), x_rows, _p(row_token), _live(offsets), _p(o["codes"]),
-                                  _p(o["scales"]), _p(o["row_scale"]), _p(o["values"]), _raw_stream(d)),
-           "moe_quantize_nvfp4")
+    _check(lib.moe_quantize_nvfp4(rows, cols, dt, x.data_ptr(), x_rows, _p(row_token), _live(offsets),
+                                  o["codes"].data_ptr(), o["scales"].data_ptr(), _p(o["row_scale"]), _p(o["values"]),
+                                  _raw_stream(d)), "moe_quantize_nvfp4")
     return o
 
 
@@ -552,8 +554,8 @@ def swiglu_quantize_nvfp4(gu: torch.Tensor, clamp: float = 0.0, clamp_mode="prea
         with _on(d, stream):
             return swiglu_quantize_nvfp4(gu, clamp, clamp_mode, offsets, row_scaled, values, out)
     o = _nvfp4_outputs(rows, cols, gu, row_scaled, values, out)
-    _check(lib.moe_swiglu_quantize_nvfp4(rows, cols, dt, _p(gu), clamp, CLAMP_MODES[clamp_mode], _live(offsets),
-                                         _p(o["codes"]), _p(o["scales"]), _p(o["row_scale"]), _p(o["values"]),
+    _check(lib.moe_swiglu_quantize_nvfp4(rows, cols, dt, gu.data_ptr(), clamp, CLAMP_MODES[clamp_mode], _live(offsets),
+                                         o["codes"].data_ptr(), o["scales"].data_ptr(), _p(o["row_scale"]), _p(o["values"]),
                                          _raw_stream(d)), "moe_swiglu_quantize_nvfp4")
     return o
 
@@ -568,9 +570,9 @@ def swiglu(gu: torch.Tensor, clamp: float = 0.0, clamp_mode="preact", offsets: O
         with _on(d, stream):
             return swiglu(gu, clamp, clamp_mode, offsets, h)
     if h is None:
-        h = gu.new_empty((rows, F))
-    _check(lib.moe_swiglu(rows, F, dt, _p(gu), clamp, CLAMP_MODES[clamp_mode], _live(offsets), _p(h), _raw_stream(d)),
-           "moe_swiglu")
+        h = gu.new_empty(rows, F)
+    _check(lib.moe_swiglu(rows, F, dt, gu.data_ptr(), clamp, CLAMP_MODES[clamp_mode], _live(offsets), h.data_ptr(),
+                          _raw_stream(d)), "moe_swiglu")
     return h
 
 
@@ -600,9 +602,10 @@ def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, row_weight: Optional[tor
     if hw is None and need_hw:
         hw = torch.empty_like(dh)
     if drw is None and need_drow_weight:
-        drw = gu.new_empty((rows,), dtype=torch.float32)
-    _check(lib.moe_swiglu_backward(rows, F, dt, _p(gu), _p(dh), _p(row_weight), clamp, CLAMP_MODES[clamp_mode],
-                                   _live(offsets), _p(dgu), _p(hw), _p(drw), _raw_stream(d)), "moe_swiglu_backward")
+        drw = gu.new_empty(rows, dtype=torch.float32)
+    _check(lib.moe_swiglu_backward(rows, F, dt, gu.data_ptr(), dh.data_ptr(), _p(row_weight), clamp,
+                                   CLAMP_MODES[clamp_mode], _live(offsets), dgu.data_ptr(), _p(hw), _p(drw),
+                                   _raw_stream(d)), "moe_swiglu_backward")
     return dict(dgu=dgu, hw=hw, drow_weight=drw)
 
 
