@@ -8,14 +8,31 @@
 //   TN  dW[e] (+)= sum_{r in e} dy[r, :]^T a[r, :]            (weight gradient)
 //
 // NT and NN put the weights on the MMA's M side and the tokens on its N side:
-// a tile is 128 output features x up to BT tokens of one group, and its MMAs
-// run with N = the tile's tokens rounded up to 16.  A ragged group therefore
-// pads no MMA rows (with the tokens on the M side every group pads to 128),
-// weights are read once per BT tokens, and for a handful of tokens the MMA is
-// small and the kernel is a pure stream of the weights through the stage
-// ring.  TN puts dy's features on M, a's on N and reduces over the group's
-// rows; both operands are read as they lie (MN-major tiles), nothing is
+// a tile is 128 output features (a CTA pair: 256) x up to BT tokens of one
+// group, and its MMAs run with N = the tile's tokens rounded up to 16 (32).  A
+// ragged group therefore pads no MMA rows (with the tokens on the M side every
+// group pads to 128), weights are read once per BT tokens, and for a handful of
+// tokens the MMA is small and the kernel is a pure stream of the weights through
+// the stage ring.  TN puts dy's features on M, a's on N and reduces over the
+// group's rows; both operands are read as they lie (MN-major tiles), nothing is
 // transposed in memory.
+//
+// Two shapes.  Up to 64 rows a group on average: single CTAs, 64-token tiles and
+// eight 16 KB weight stages.  Above: 2-CTA pairs (cta_group::2) of 256 x 256
+// tiles, each CTA with its own 128 features and half of the tokens.  A single
+// CTA's 128 x 256 tile needs 96 bytes a cycle and SM from L2 at the MMAs' rate and
+// got about 60; the pair needs 64 (512 rows a group x 4096 x 1536: 96 -> 87 us,
+// tensor pipe 65 -> 80% of active cycles).
+//
+// Measured (B200, 1 kW limit; cool clocks / after a second of the same call):
+//   16 rows x 4096 x 28672 over 8 groups      284 us = 6.6 TB/s, a copy's rate
+//   15001 x 8192 x 2048 over 64 groups        498-520 / 633 us (DRAM 5 TB/s and
+//                                             0.97 PFLOP/s at once, 1.4 GHz)
+//   65536 x 4096 x 1536 over 128 (NN)         660 / 880 us, tensor pipe 90%
+//   8192 rows, dW 8 x 4096 x 14336 (TN)       700 / 820 us, tensor pipe 84%
+// All of the last three are held by the power limit: the clock falls to 1.2-1.4
+// GHz, and below after a while.  One cuBLAS product of the second's and third's
+// sizes (a single weight matrix): 388 and 557 us.
 //
 // A K-major tile lies in shared memory as rows of 64 reduction elements (128
 // bytes, 128-byte swizzle); an MN-major tile as boxes of 64 features x 64
@@ -708,8 +725,9 @@ moe_status launch_grouped_bf16(const MoEGrouped &g, const void *a, const int32_t
   p.out = y;
   p.out_f32 = g.out_dtype == MOE_F32;
   p.status = status;
-  // few rows a group: narrow token tiles leave the ring eight 16 KB weight
-  // stages instead of four
+  // few rows a group: single CTAs with narrow token tiles.  8 / 16 / 64 / 96 / 128
+  // rows in each of 32 groups x 4096 x 2048: 91 / 94 / 97 / 112 / 116 us so, with
+  // pairs 97 / 99 / 103 / 106 / 109.
   const bool narrow = g.rows <= 64l * g.groups;
   if (transposed) return narrow ? launch<NN, 64>(p, w, a, s) : launch<NN, 256>(p, w, a, s);
   return narrow ? launch<NT, 64>(p, w, a, s) : launch<NT, 256>(p, w, a, s);

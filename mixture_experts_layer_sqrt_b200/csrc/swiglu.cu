@@ -11,9 +11,11 @@
 // With the clamp at L, a clipped g or u (|v| > L) gets no gradient; in the
 // output mode h is clipped and a clipped h passes none.
 //
-// Streams: forward 3, backward 6 elements moved per hidden element.  The
-// arithmetic (one exponential, one division) stays under the copy time for
-// bf16.  A warp (or, with few rows, a block of eight) per row, 16-byte loads.
+// Streams: forward 3, backward 6 elements moved per hidden element.  A warp (or,
+// with few rows, a block of eight) per row, 16-byte loads, the next piece loaded
+// ahead.  Measured (B200, bf16): backward 65536 x 1536 203 us = 5.95 TB/s (a copy:
+// 6.5; 55 instructions an element with the accurate exponential took 243 us);
+// forward 16384 x 4096 75 us = 5.3 TB/s.
 #include "act.cuh"
 #include "kernels.h"
 
