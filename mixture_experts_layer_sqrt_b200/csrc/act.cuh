@@ -15,8 +15,8 @@ __device__ __forceinline__ float clip(float v, float limit) { return v < -limit 
 __device__ __forceinline__ float sigmoid_f32(float g) { return __frcp_rn(1.0f + expf(-g)); }
 
 // For bf16 gradients: the hardware's exponential and reciprocal, within 2^-20 of
-// the value for |g| < 10, against the 2^-8 of the store (18 instead of 56
-// instructions an element, the backward pass 61 -> 44 us at 16384 x 1536).
+// the value for |g| < 10, against the 2^-8 of the store (27 instead of 56
+// instructions an element, the backward pass 69 -> 54 us at 16384 x 1536).
 __device__ __forceinline__ float sigmoid_fast(float g) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
