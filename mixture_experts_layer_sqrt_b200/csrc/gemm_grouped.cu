@@ -21,7 +21,7 @@
 // eight 16 KB weight stages.  Above: 2-CTA pairs (cta_group::2) of 256 x 256
 // tiles, each CTA with its own 128 features and half of the tokens.  A single
 // CTA's 128 x 256 tile needs 96 bytes a cycle and SM from L2 at the MMAs' rate and
-// got about 60; the pair needs 64 (512 rows a group x 4096 x 1536: 96 -> 87 us,
+// got about 50; the pair needs 64 (512 rows a group x 4096 x 1536: 96 -> 87 us,
 // tensor pipe 65 -> 80% of active cycles).
 //
 // Measured (B200, 1 kW limit; cool clocks / after a second of the same call):

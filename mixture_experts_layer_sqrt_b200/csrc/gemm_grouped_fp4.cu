@@ -30,8 +30,7 @@
 // Measured (B200): 48 rows x 4096 x 2048 over 384 groups 46 us (227 MB of weights
 // at 4.9 TB/s; the last tiles, with five or six a CTA, and the start take the
 // rest); 49152 rows 386-400 us (2.1 GB, 5.4 TB/s), 471 us after a second under the
-// power limit; 8192 rows x 4096 x 4096 over 4 groups 88 us = 3.1 PFLOP/s, where a
-// stage's 256 elements are copied at about 64 bytes a cycle and SM.
+// power limit; 8192 rows x 4096 x 4096 over 4 groups 88 us = 3.1 PFLOP/s.
 #include <cudaTypedefs.h>
 #include <limits.h>
 

