@@ -2,6 +2,8 @@
 the most groups, offsets out of range, sizes whose element offsets pass 32 bits,
 base addresses aligned to 16 bytes only, inputs and offsets that change under a
 captured graph, and the checked build's refusal of bad indices."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -248,3 +250,48 @@ def test_checked_build_refuses_bad_offsets_nvfp4_and_row_maps(BC):
     for k in q:
         assert torch.equal(q[k][[0, 2]], want[k]), k
     assert lib.moe_checked_violations() == 0
+
+
+# ------------------------------------------------------------------ two host threads at once
+
+@pytest.mark.gpu
+def test_different_operators_from_two_threads_at_once(B):
+    offs = torch.tensor([0, 40, 40, 130, 137], dtype=torch.int32, device=CUDA)
+    gen = torch.Generator().manual_seed(5)
+    x = torch.randn(137, 256, generator=gen).to(CUDA, torch.bfloat16)
+    w = torch.randn(4, 192, 256, generator=gen).to(CUDA, torch.bfloat16)
+    dy = torch.randn(137, 192, generator=gen).to(CUDA, torch.bfloat16)
+    q, qw = B.quantize_nvfp4(x), B.quantize_nvfp4(w.reshape(-1, 256))
+    calls = [
+        lambda s: B.grouped_matmul(x, w, offs, stream=s),
+        lambda s: B.grouped_wgrad(dy, x, offs, stream=s),
+        lambda s: B.grouped_matmul(dy, w, offs, transposed=True, stream=s),
+        lambda s: B.grouped_matmul_nvfp4(q["codes"], q["scales"], qw["codes"].reshape(4, 192, 128),
+                                         qw["scales"].reshape(4, 192, 16), offs, q["row_scale"],
+                                         qw["row_scale"].reshape(4, 192), stream=s),
+        lambda s: B.swiglu_quantize_nvfp4(x, values=True, stream=s)["values"],
+    ]
+    # rows outside the groups do not exist here (the offsets cover all), so whole outputs compare
+    want = [f(None) for f in calls]
+    torch.cuda.synchronize()
+    streams, got, errors = [torch.cuda.Stream() for _ in range(2)], [[], []], []
+
+    def run(i):
+        try:
+            for j in range(20):
+                k = (j * (i + 1) + i) % len(calls)
+                got[i].append((k, calls[k](streams[i])))
+        except Exception as e:  # noqa: BLE001 - handed to the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for results in got:
+        assert len(results) == 20
+        for k, r in results:
+            assert torch.equal(r, want[k]), k
