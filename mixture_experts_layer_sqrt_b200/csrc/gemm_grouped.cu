@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (PAIR) ptx::mbar_arrive_cluster(ptx::map_to_rank(&sm.tmem_empty[acc], lead));
+          if (PAIR) arrive_cluster_relaxed(ptx::map_to_rank(&sm.tmem_empty[acc], lead));
           else ptx::mbar_arrive(&sm.tmem_empty[acc]);
         }
       }

@@ -56,6 +56,16 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// The epilogue's hand-back of an accumulator to the pair's leader.  It publishes
+// no memory: the TMEM reads before it are complete (tcgen05.wait::ld) and ordered
+// by tcgen05.fence::before_thread_sync.  A releasing arrive at cluster scope would
+// wait for all of the tile's global stores as well, about 2500 cycles a tile
+// (weight gradient of 110 rows, 6 x 6128 x 3768: 127 -> 88 us; 23203 rows x 1792
+// x 96: 51 -> 45; where the reduction hides it, as in the large products, equal).
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Used while winding down: copies and MMAs already issued must land first.
 __device__ __forceinline__ void drain_bar(uint64_t *bar, uint32_t parity, int *status) {
   const uint64_t t0 = ptx::globaltimer_ns();
