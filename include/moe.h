@@ -29,7 +29,8 @@
  *    word at the start of `ws`; read them with moe_check_device_status().
  *  - Nothing about a layer is kept between calls.  The library's only global
  *    state is a launch counter, the fixed scratch array of
- *    moe_dispatch_noalloc and, in the checked build, its violation counters.
+ *    moe_dispatch_noalloc, the status words of moe_status_workspace and, in
+ *    the checked build, its violation counters.
  */
 #ifndef MOE_B200_H
 #define MOE_B200_H
@@ -151,6 +152,15 @@ uint64_t moe_checked_violations(void);
  * start of `ws` (any workspace passed to the calls above).  Returns MOE_OK or
  * MOE_ERR_DEVICE_TIMEOUT; MOE_ERR_CUDA if the stream reports an error. */
 moe_status moe_check_device_status(void *ws, moe_stream_t stream);
+
+/* A workspace of the library's own on the current device, for the calls that
+ * need no more than a status word (moe_grouped_matmul, moe_grouped_wgrad,
+ * moe_grouped_matmul_nvfp4) and have none from the caller: *ws its device
+ * address, the same until the process exits, *ws_bytes its size (256; both host
+ * pointers).  All streams and threads may use it at once: the kernels only
+ * record a timeout there, so moe_check_device_status of it tells whether any
+ * call that used it and that `stream` has waited for ran out of time. */
+moe_status moe_status_workspace(void **ws, size_t *ws_bytes);
 
 /* Exercises the timeout path of the kernels' bounded waits: launches one
  * block that waits, with the same bounded wait the GEMM pipelines use, on an

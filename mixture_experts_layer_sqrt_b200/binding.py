@@ -69,6 +69,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_checked_build": (I, []),
         "moe_checked_violations": (c_uint64, []),
         "moe_check_device_status": (I, [P, P]),
+        "moe_status_workspace": (I, [POINTER(P), POINTER(S)]),
         "moe_route_workspace_size": (S, [cfgp, I]),
         "moe_route_topk": (I, [cfgp, I, P, wp, P, P, P, P, S, P]),
         "moe_dispatch_workspace_size": (S, [cfgp, I]),
@@ -105,7 +106,7 @@ lib = load_library()
 # Every function the header declares (checked by the tests).
 EXPORTS = ("moe_status_string", "moe_version", "moe_expert_capacity", "moe_launch_count", "moe_checked_build",
            "moe_checked_violations",
-           "moe_check_device_status", "moe_route_workspace_size", "moe_route_topk", "moe_dispatch_workspace_size",
+           "moe_check_device_status", "moe_status_workspace", "moe_route_workspace_size", "moe_route_topk", "moe_dispatch_workspace_size",
            "moe_dispatch", "moe_dispatch_noalloc", "moe_grouped_swiglu_workspace_size", "moe_expert_workspace_size",
            "moe_expert_gate_up", "moe_expert_down", "moe_grouped_swiglu", "moe_combine",
            "moe_workspace_size", "moe_forward", "moe_forward_profiled", "moe_selftest_wait_timeout",
@@ -167,7 +168,8 @@ def make_weights(t: Dict[str, Optional[torch.Tensor]]) -> MoEWeights:
 
 
 def workspace(nbytes: int, device=None) -> torch.Tensor:
-    """A zeroed device workspace (the status word must start at zero)."""
+    """A zeroed device workspace (the status word must start at zero).  A stage called without
+    one makes its own and drops it, with its status word: pass one to check_device_status it."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
 
 
@@ -356,6 +358,22 @@ def _raw_stream(d: int) -> int:
     return torch._C._cuda_getCurrentRawStream(d)
 
 
+_status_ws: Dict[int, tuple] = {}
+
+
+def _workspace_of(ws: Optional[torch.Tensor], d: int):
+    """(address, bytes) of ws, or without one of the library's own on device d (the current one),
+    which check_device_status() reads."""
+    if ws is not None:
+        return ws.data_ptr(), ws.numel()
+    own = _status_ws.get(d)
+    if own is None:
+        p, n = c_void_p(), c_size_t()
+        _check(lib.moe_status_workspace(ctypes.byref(p), ctypes.byref(n)), "moe_status_workspace")
+        own = _status_ws[d] = (p.value, n.value)
+    return own
+
+
 def _act_dtype(t: torch.Tensor, what: str) -> int:
     if t.dtype not in _DTYPE_OF:
         raise ValueError(f"{what}: expected float32 or bfloat16, got {t.dtype}")
@@ -391,7 +409,8 @@ def grouped_matmul(a: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Ten
                    stream=None) -> torch.Tensor:
     """Rows of group e times w[e]: y = a w[e]^T with w [E, N, K], or y = a w[e] with w [E, K, N]
     when transposed (the input gradient of a product stored as [E, K, N]).  `out`: "bf16" or
-    "f32" (by default the type of y, or of a)."""
+    "f32" (by default the type of y, or of a).  Without ws the status of this and the two products
+    below is that of check_device_status()."""
     _matrix(a, 2, "a")
     _matrix(w, 3, "w")
     rows, K = a.shape
@@ -409,10 +428,9 @@ def grouped_matmul(a: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Ten
             return grouped_matmul(a, w, offsets, transposed, row_weight, y, out, ws)
     if y is None:
         y = a.new_empty(rows, N, dtype=odt)
-    if ws is None:
-        ws = workspace(256, a.device)
+    ws, ws_bytes = _workspace_of(ws, d)
     _check(lib.moe_grouped_matmul(g, a.data_ptr(), _p(offsets), w.data_ptr(), transposed, _p(row_weight), y.data_ptr(),
-                                  ws.data_ptr(), ws.numel(), _raw_stream(d)), "moe_grouped_matmul")
+                                  ws, ws_bytes, _raw_stream(d)), "moe_grouped_matmul")
     return y
 
 
@@ -440,10 +458,9 @@ def grouped_wgrad(dy: torch.Tensor, a: torch.Tensor, offsets: Optional[torch.Ten
             return grouped_wgrad(dy, a, offsets, dw, accumulate, out, ws)
     if dw is None:
         dw = a.new_empty(E, N, K, dtype=odt)
-    if ws is None:
-        ws = workspace(256, a.device)
+    ws, ws_bytes = _workspace_of(ws, d)
     _check(lib.moe_grouped_wgrad(g, dy.data_ptr(), a.data_ptr(), _p(offsets), accumulate, dw.data_ptr(),
-                                 ws.data_ptr(), ws.numel(), _raw_stream(d)), "moe_grouped_wgrad")
+                                 ws, ws_bytes, _raw_stream(d)), "moe_grouped_wgrad")
     return dw
 
 
@@ -474,12 +491,10 @@ def grouped_matmul_nvfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
                                         ws)
     if y is None:
         y = a.new_empty(rows, N, dtype=odt)
-    if ws is None:
-        ws = workspace(256, a.device)
+    ws, ws_bytes = _workspace_of(ws, d)
     _check(lib.moe_grouped_matmul_nvfp4(g, a.data_ptr(), a_scales.data_ptr(), _p(a_row_scale), _p(offsets),
                                         w.data_ptr(), w_scales.data_ptr(), _p(w_row_scale), _p(row_weight),
-                                        y.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(d)),
-           "moe_grouped_matmul_nvfp4")
+                                        y.data_ptr(), ws, ws_bytes, _raw_stream(d)), "moe_grouped_matmul_nvfp4")
     return y
 
 
@@ -649,7 +664,15 @@ def selftest_wait_timeout(ws: torch.Tensor, stream=None):
     _check(lib.moe_selftest_wait_timeout(_p(ws), ws.numel(), _stream(stream)), "moe_selftest_wait_timeout")
 
 
-def check_device_status(ws: torch.Tensor, stream=None):
+def check_device_status(ws: Optional[torch.Tensor] = None, stream=None):
+    """Waits for the stream (by default the current one), then raises if a kernel that used ws
+    gave up a bounded wait, and clears the status.  Without ws: the grouped products that were
+    called without one, on the stream's device."""
+    if ws is None:
+        d = stream.device.index if stream is not None else torch.cuda.current_device()
+        with torch.cuda.device(d):
+            _check(lib.moe_check_device_status(_workspace_of(None, d)[0], _stream(stream)), "device status")
+        return
     _check(lib.moe_check_device_status(_p(ws), _stream(stream)), "device status")
 
 

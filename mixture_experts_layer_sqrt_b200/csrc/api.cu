@@ -4,6 +4,7 @@
 #include <stdlib.h>
 
 #include <atomic>
+#include <mutex>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -16,6 +17,12 @@ static std::atomic<uint64_t> g_launches{0};
 void count_launch(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 
 namespace {
+
+// moe_status_workspace: in every GPU's own copy of the library, zero when loaded.
+__device__ __align__(256) int g_status_ws[kStatusBytes / sizeof(int)];
+constexpr int kMaxDevices = 64;
+std::mutex g_status_mu;
+void *g_status_ptr[kMaxDevices] = {};
 
 inline size_t act_size(const MoEConfig &c) { return c.act_dtype == MOE_F32 ? 4 : 2; }
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -261,6 +268,27 @@ moe_status moe_check_device_status(void *ws, moe_stream_t stream) {
     MOE_CUDA_TRY(cudaStreamSynchronize(s));
     return MOE_ERR_DEVICE_TIMEOUT;
   }
+  return MOE_OK;
+}
+
+moe_status moe_status_workspace(void **ws, size_t *ws_bytes) {
+  if (!ws || !ws_bytes) return MOE_ERR_INVALID_ARG;
+  int dev = -1;
+  MOE_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lock(g_status_mu);
+  if (!g_status_ptr[dev]) {
+    // the first look-up may load the library's code: allowed while this thread captures a stream
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    MOE_CUDA_TRY(cudaThreadExchangeStreamCaptureMode(&mode));
+    void *p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_status_ws);
+    MOE_CUDA_TRY(cudaThreadExchangeStreamCaptureMode(&mode));
+    MOE_CUDA_TRY(e);
+    g_status_ptr[dev] = p;
+  }
+  *ws = g_status_ptr[dev];
+  *ws_bytes = kStatusBytes;
   return MOE_OK;
 }
 
