@@ -49,8 +49,8 @@
 //   warps 2-9 epilogue: TMEM lane = output feature (TN: warps 2-5)
 //   warp 6    TN: clears the lines above and hands the stage on to the MMAs
 //
-// Every wait is bounded (2 s, then MOE_ERR_DEVICE_TIMEOUT in the status word
-// and an orderly wind down).
+// Every wait is bounded (2 s, and 4 us for every stage that passes meanwhile; then
+// MOE_ERR_DEVICE_TIMEOUT in the status word and an orderly wind down).
 #include <cudaTypedefs.h>
 #include <limits.h>
 
@@ -423,13 +423,16 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   } else if (MODE == TN && warp == kClearWarp) {
     // ================================================= lines of other rows (TN)
     uint32_t at = 0, phase = 0;  // blocks so far; next phase of each stage's landed barrier
+    uint32_t since = 0;          // blocks and epilogues (as 16 blocks) since the last partial block
     for (int t = unit; t < total; t += n_units) {
       const Tile tl = tile_of(t);
       const int left = tl.red % BK;
       at += (tl.red + BK - 1) / BK;
+      since += (tl.red + BK - 1) / BK + 16;
       if (left == 0) continue;
       const int s = (at - 1) % STAGES;
-      if (!warp_wait(&sm.landed[s], phase >> s & 1, &sm.abort, p.status)) break;
+      if (!warp_wait(&sm.landed[s], phase >> s & 1, &sm.abort, p.status, since)) break;
+      since = 0;
       __syncwarp();
       // lines [left, the MMAs' last) of every box
       uint8_t *a = stage_a + s * A_BYTES + left * 128, *b = stage_b + s * C::B_BYTES + left * 128;
@@ -464,7 +467,9 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
       const float w0 = MODE != TN ? row_factor(store, tl.row0, tl.count, group * 32) : 1.0f;
       if (have) {
         ++i;
-        if (!all_agree<3, 32 * kEpiWarps<MODE>>(warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status))) break;
+        if (!all_agree<3, 32 * kEpiWarps<MODE>>(
+                warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status, (tl.red + BK - 1) / BK)))
+          break;
         ptx::tc_fence_after();
       }
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;

@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = tl.blk * BM + q * 32 + lane;
       const float w0 = row_factor(store, tl.row0, tl.count, group * 32);
       const float wn = p.rw && n < p.N ? p.rw[(long)tl.e * p.N + n] : 1.0f;
-      if (!all_agree<3, 128 * kEpiGroups>(warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status))) break;
+      if (!all_agree<3, 128 * kEpiGroups>(warp_wait(&sm.tmem_full[acc], aph, &sm.abort, p.status, kb1 - kb0))) break;
       ptx::tc_fence_after();
       const uint32_t tbase = tmem_base + lane_addr + acc * BT;
       if (p.split > 1) put_part_columns(parts, tbase, tl.count, q, group, kEpiGroups);

@@ -14,17 +14,25 @@ namespace grouped {
 constexpr int MAX_E = 1024;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr uint64_t kDrainLimitNs = 200000000ull;  // 0.2 s
+constexpr uint64_t kStepNs = 4000;                // a stage of a reduction takes 0.2-0.3 us, 1.5 with the SM's share of HBM
 
 // Bounded wait; false if the CTA is aborting (this thread may have started
-// it).  The thread sleeps on the barrier with a suspend-time hint: measured
-// 2-12% faster over the grouped products than polling it.
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int *abort_flag, int *status) {
+// it).  `steps`: stages of a reduction that pass meanwhile, for the waits that span
+// more than one: an epilogue waits for a whole reduction, the clearing warp of a
+// weight gradient for the next tile with a partial block.  600 million rows of 8
+// columns in one tile take 2.3 s, a healthy launch; so the limit grows by kStepNs a
+// stage.  The waits for one stage keep the 2 s.  (A count of issued stages that
+// restarts the limit cost 0.5-1% of every product.)  The thread sleeps on the
+// barrier with a suspend-time hint: measured 2-12% faster over the grouped products
+// than polling it.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int *abort_flag, int *status,
+                                         uint32_t steps = 0) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   for (;;) {
     if (ptx::mbar_try_wait_sleep(bar, parity, ptx::kWaitHintNs)) return true;
     if (*(volatile int *)abort_flag) return false;
-    if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+    if (ptx::globaltimer_ns() - t0 > kWaitLimitNs + steps * kStepNs) {
       *(volatile int *)abort_flag = 1;
       atomicExch(status, kDevTimeout);
       return false;
@@ -33,8 +41,9 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int *ab
 }
 
 // Warp-uniform wait: every lane waits, and all go on or none.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *abort_flag, int *status) {
-  const bool ok = wait_bar(bar, parity, abort_flag, status);
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *abort_flag, int *status,
+                                          uint32_t steps = 0) {
+  const bool ok = wait_bar(bar, parity, abort_flag, status, steps);
   return __all_sync(0xffffffffu, ok);
 }
 
