@@ -306,8 +306,11 @@ moe_status moe_grouped_swiglu(const MoEConfig *cfg, int rows, const void *x_perm
  * Group e owns the rows expert_offsets[e] .. expert_offsets[e+1] - 1 (device
  * int32 [groups + 1], not decreasing, as moe_dispatch writes it; NULL = one
  * group of all rows, groups = 1).  Offsets are kept within [0, rows] before
- * use.  A group may be empty.  Output rows before the first and from the last
- * offset on are left as they were.  Sums are accumulated in fp32. */
+ * use.  Decreasing offsets are an error of the caller's that is not reported:
+ * nothing out of range is read or written, but a row may be computed for several
+ * groups, and a product whose groups overlap too often writes nothing.  A group
+ * may be empty.  Output rows before the first and from the last offset on are
+ * left as they were.  Sums are accumulated in fp32. */
 typedef struct {
   int groups;          /* E, 1..1024 */
   int rows;            /* rows of the token matrices; bounds every offset */

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads<MODE>, 1)
   if (warp == 2 && (MODE != TN || kChecked)) {
     // TN needs no tile list (every group has m_blocks * n_blocks tiles), but
     // the same check of the offsets
-    const bool ok = scan_tiles(sm.off, p.E, p.tile, sm.start);
+    const bool ok = scan_tiles(sm.off, p.E, p.rows, p.tile, sm.start);
     if (kChecked && !ok && lane == 0 && blockIdx.x == 0) note_violation();
     if (kChecked && MODE == TN && lane == 0) sm.start[0] = ok ? 0 : 1;
   }

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) grouped_f32(int rows, int N, int K, 
     load_offsets(offsets, rows, E, off);
     __syncthreads();
     if (threadIdx.x < 32) {
-      const bool ok = scan_tiles(off, E, BM, start);
+      const bool ok = scan_tiles(off, E, rows, BM, start);
       if (kChecked && !ok && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) note_violation();
     }
     __syncthreads();

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   load_offsets(p.offsets, p.rows, p.E, sm.off);
   __syncthreads();
   if (warp == 2) {
-    const bool ok = scan_tiles(sm.off, p.E, p.tile, sm.start);
+    const bool ok = scan_tiles(sm.off, p.E, p.rows, p.tile, sm.start);
     if (kChecked && !ok && lane == 0 && blockIdx.x == 0) note_violation();
   }
   ptx::tc_fence_before();

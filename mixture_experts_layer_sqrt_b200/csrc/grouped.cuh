@@ -144,8 +144,8 @@ struct Ring {
 // barrier): one load latency whatever E, where a warp that scanned them from
 // global memory took 10 us for 384 groups.  They are kept within [0, rows], so
 // that offsets out of range cannot lead to an access out of range.  offsets ==
-// null: one group of all rows.  Checked build: a negative or decreasing offset
-// leaves all groups empty (scan_tiles).
+// null: one group of all rows.  The checked build keeps negative ones for scan_tiles
+// to find.
 __device__ __forceinline__ void load_offsets(const int32_t *offsets, int rows, int E, int *off) {
 #pragma unroll 4
   for (int e = threadIdx.x; e <= E; e += blockDim.x) {
@@ -160,16 +160,19 @@ __device__ __forceinline__ int group_rows(const int *off, int e) {
 }
 
 // One warp: start[e] = sum over e' < e of ceil(rows_e' / tile_rows), e = 0..E
-// (the last entry is the total).  Checked build: false if the offsets are bad.
-__device__ __forceinline__ bool scan_tiles(int *off, int E, int tile_rows, int *start) {
+// (the last entry is the total).  False if the offsets are bad; then all groups are
+// empty.  Offsets that decrease make groups overlap, and overlapping groups can have
+// more tiles than the host made room for, or than an int counts (1000 groups that
+// go to and fro over a million rows): such a call does nothing.  Sums stop just
+// above the limit, so that they stay within 32 bits.  Checked build: any negative
+// or decreasing offset is bad.
+__device__ __forceinline__ bool scan_tiles(int *off, int E, int rows, int tile_rows, int *start) {
   const int lane = threadIdx.x & 31;
+  const int limit = (rows + tile_rows - 1) / tile_rows + min(rows, E);
+  bool bad = false;
   if (kChecked) {
-    bool bad = false;
     for (int e = lane; e < E; e += 32) bad |= off[e] < 0 || off[e + 1] < off[e];
-    if (__any_sync(0xffffffffu, bad)) {
-      for (int e = lane; e <= E; e += 32) off[e] = start[e] = 0;
-      return false;
-    }
+    bad = __any_sync(0xffffffffu, bad);
   }
   // a lane's groups in a row, then one scan over the lanes
   const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
@@ -177,7 +180,7 @@ __device__ __forceinline__ bool scan_tiles(int *off, int E, int tile_rows, int *
 #pragma unroll 4
   for (int e = e0; e < e1; ++e) {
     start[e] = sum;
-    sum += (group_rows(off, e) + tile_rows - 1) / tile_rows;
+    sum = min(sum + (group_rows(off, e) + tile_rows - 1) / tile_rows, limit + 1);
   }
   int incl = sum;
 #pragma unroll
@@ -188,7 +191,12 @@ __device__ __forceinline__ bool scan_tiles(int *off, int E, int tile_rows, int *
 #pragma unroll 4
   for (int e = e0; e < e1; ++e) start[e] += incl - sum;
   if (lane == 31) start[E] = incl;
-  return true;
+  bad |= __shfl_sync(0xffffffffu, incl, 31) > limit;
+  if (bad) {
+    __syncwarp();
+    for (int e = lane; e <= E; e += 32) off[e] = start[e] = 0;
+  }
+  return !bad;
 }
 
 // Largest e with start[e] * per <= t (empty groups share the next start).
