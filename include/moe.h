@@ -390,7 +390,8 @@ moe_status moe_swiglu(int rows, int F, moe_dtype dtype, const void *gu, float cl
  * dh = dy W_down (not multiplied by row_weight):
  *   dgu          [rows, 2F]: gradient of gu, row_weight included (may be gu itself)
  *   hw           [rows, F] or NULL: row_weight[r] * h[r], the operand of dW_down = dy^T hw
- *   drow_weight  [rows] float or NULL: sum over F of dh * h
+ *   drow_weight  [rows] float or NULL: sum over F of dh * h, in fp32 from h before
+ *                its rounding to dtype; each term within 10 * 2^-24 of its value
  * row_weight [rows] or NULL (= 1).  A clipped g or u gets no gradient, nor does
  * anything behind a clipped h (MOE_CLAMP_OUTPUT).  Deterministic. */
 moe_status moe_swiglu_backward(int rows, int F, moe_dtype dtype, const void *gu, const void *dh,

@@ -13,8 +13,8 @@
 //
 // Streams: forward 3, backward 6 elements moved per hidden element.  A warp (or,
 // with few rows, a block of eight) per row, 16-byte loads, the next piece loaded
-// ahead.  Measured (B200, bf16): backward 65536 x 1536 203 us = 5.95 TB/s (a copy:
-// 6.5; 55 instructions an element with the accurate exponential took 243 us);
+// ahead.  Measured (B200, bf16): backward 65536 x 1536 206 us = 5.87 TB/s (a copy:
+// 6.5; with the correctly rounded reciprocal as well it took 243 us);
 // forward 16384 x 4096 75 us = 5.3 TB/s.
 #include "act.cuh"
 #include "kernels.h"
