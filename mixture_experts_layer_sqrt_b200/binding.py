@@ -329,14 +329,28 @@ _DTYPE_OF = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
 def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
-    """The one CUDA device of the tensors."""
-    d = first.get_device()
+    """The one CUDA device of the tensors.  A tensor that autograd follows is refused: the kernels
+    work on addresses, and its gradient would be lost without a word.  (Under no_grad, and so in
+    the forward and backward of a torch.autograd.Function, nothing is followed.)"""
+    followed, d, other = torch.is_grad_enabled(), first.get_device(), None
+    if followed and first.requires_grad:
+        raise ValueError(_NO_AUTOGRAD)
+    for t in others:
+        if t is not None:
+            if followed and t.requires_grad:
+                raise ValueError(_NO_AUTOGRAD)
+            if t.get_device() != d:
+                other = t
     if d < 0:
         raise ValueError(f"expected CUDA tensors, got one on {first.device}")
-    for t in others:
-        if t is not None and t.get_device() != d:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+    if other is not None:
+        raise ValueError(f"tensors on {first.device} and {other.device}")
     return d
+
+
+_NO_AUTOGRAD = ("a tensor requires grad, but these operators record no gradient: call them under torch.no_grad() or "
+                "inside a torch.autograd.Function, with grouped_matmul(transposed=True), grouped_wgrad and "
+                "swiglu_backward for the gradients")
 
 
 def _elsewhere(d: int, stream) -> bool:
