@@ -315,13 +315,16 @@ typedef struct {
   int groups;          /* E, 1..1024 */
   int rows;            /* rows of the token matrices; bounds every offset */
   int n;               /* output columns (wgrad: columns of dy), a multiple of 8 */
-  int k;               /* reduction length (wgrad: columns of a), a multiple of 8; NVFP4: of 32 */
+  int k;               /* reduction length (wgrad: columns of a), a multiple of 8; NVFP4: of 32,
+                          and of 256 beyond 2^26 */
   moe_dtype dtype;     /* operands: MOE_F32 (CUDA cores), MOE_BF16, MOE_NVFP4 (tensor cores) */
   moe_dtype out_dtype; /* MOE_F32, or MOE_BF16 (not from F32 operands): one rounding of the fp32 result */
 } MoEGrouped;
 
 /* Bytes of workspace the three products below need (their device status
- * word); 0 for sizes they refuse. */
+ * word); 0 for a MoEGrouped that is not valid, which they refuse.  Of the valid
+ * ones they refuse with MOE_ERR_UNSUPPORTED fp32 outputs from fp32 operands with
+ * more than 4194240 columns (wgrad: k). */
 size_t moe_grouped_workspace_size(const MoEGrouped *g);
 
 /* y[r, :] = row_weight[r] * (a[r, :] W[e]^T)   w [E, n, k], transposed = 0

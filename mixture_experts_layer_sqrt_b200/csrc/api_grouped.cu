@@ -20,6 +20,8 @@ moe_status validate(const MoEGrouped *g) {
   if (g->dtype == MOE_F32 && g->out_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
   if (g->groups > 1024) return MOE_ERR_UNSUPPORTED;
   if (g->n % 8 || g->k % (g->dtype == MOE_NVFP4 ? 32 : 8)) return MOE_ERR_UNSUPPORTED;  // 16-byte rows
+  // scale rows of other lengths are addressed by 32-bit offsets within a tile (gemm_grouped_fp4.cu)
+  if (g->dtype == MOE_NVFP4 && g->k % 256 && g->k > 1 << 26) return MOE_ERR_UNSUPPORTED;
   if (g->rows > INT_MAX / 2 || g->n > INT_MAX / 2 || g->k > INT_MAX / 2) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -621,7 +621,6 @@ moe_status launch_grouped_nvfp4(const MoEGrouped &g, const void *a, const void *
   // up to 192 tokens 38 / 37 / 40 / 42
   const bool narrow = g.rows <= 64l * g.groups;
   const bool sf_tma = g.k % 256 == 0;
-  if (!sf_tma && g.k > 1 << 26) return MOE_ERR_UNSUPPORTED;  // a tile's scale offsets in 32 bits
   if (narrow) return sf_tma ? launch<64, true>(p, a, w, s) : launch<64, false>(p, a, w, s);
   return sf_tma ? launch<192, true>(p, a, w, s) : launch<192, false>(p, a, w, s);
 }
