@@ -338,8 +338,12 @@ moe_status moe_grouped_matmul(const MoEGrouped *g, const void *a, const int32_t 
 /* dw[e] = sum over the rows r of group e of dy[r, :]^T a[r, :]
  *   dy [rows, n], a [rows, k], dw [E, n, k] out_dtype
  * An empty group's dw is zero.  accumulate != 0: the sum is added to dw (in
- * fp32, rounded once) and an empty group's dw is left as it is.  Each element
- * is one sum in row order: deterministic. */
+ * fp32, rounded once) and an empty group's dw is left as it is.
+ * Deterministic: the same sizes give the same bits on the same kind of device.
+ * An element is formed in row order, or with bf16 operands and few, long groups
+ * as the sum of 2 or 4 such sums over runs of the group's rows, in their order; how
+ * many is chosen from rows, groups, n, k and the number of SMs.  (The other products
+ * cut long reductions likewise, into up to 8 runs of k.) */
 moe_status moe_grouped_wgrad(const MoEGrouped *g, const void *dy, const void *a, const int32_t *expert_offsets,
                              int accumulate, void *dw, void *ws, size_t ws_bytes, moe_stream_t stream);
 
@@ -395,6 +399,7 @@ moe_status moe_swiglu(int rows, int F, moe_dtype dtype, const void *gu, float cl
  *   hw           [rows, F] or NULL: row_weight[r] * h[r], the operand of dW_down = dy^T hw
  *   drow_weight  [rows] float or NULL: sum over F of dh * h, in fp32 from h before
  *                its rounding to dtype; each term within 10 * 2^-24 of its value
+ *                (g > -87; a bf16 row's sigmoid is 0 below)
  * row_weight [rows] or NULL (= 1).  A clipped g or u gets no gradient, nor does
  * anything behind a clipped h (MOE_CLAMP_OUTPUT).  Deterministic. */
 moe_status moe_swiglu_backward(int rows, int F, moe_dtype dtype, const void *gu, const void *dh,

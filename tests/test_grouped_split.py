@@ -82,3 +82,16 @@ def test_product_in_parts(B, sizes, N, K, out, transposed):
     got = _np(y)
     _check(got, ref, mag, K, out, "y")
     assert (got[:2] == 7.0).all() and (got[-5:] == 7.0).all(), "rows of no group were written"
+
+
+@pytest.mark.parametrize("sizes,N,K", [([8200], 264, 136), ([4500, 0, 40, 4000], 72, 136)])
+def test_parts_give_the_same_bits_every_time(B, sizes, N, K):
+    rows = sum(sizes)
+    dy, a = _rand(1, (rows, N), "bf16").to(CUDA), _rand(2, (rows, K), "bf16").to(CUDA)
+    offs = torch.tensor(_offsets(sizes), dtype=torch.int32, device=CUDA)
+    first, streams = B.grouped_wgrad(dy, a, offs, out="f32"), [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [B.grouped_wgrad(dy, a, offs, out="f32", stream=s) for _ in range(5) for s in streams]  # side by side
+    torch.cuda.synchronize()
+    for g in got:
+        assert torch.equal(g, first)
