@@ -358,13 +358,17 @@ def _elsewhere(d: int, stream) -> bool:
     return stream is not None or d != torch.cuda.current_device()
 
 
-def _on(d: int, stream):
+def _on(d: int, stream, *tensors: Optional[torch.Tensor]):
     """The context of device d and `stream`, so that what is allocated for a call belongs to
-    the stream that uses it."""
+    the stream that uses it.  The call's tensors are recorded as used there: one that the caller
+    drops before the stream gets to the call keeps its memory until then."""
     if stream is None:
         return torch.cuda.device(d)
     if stream.device.index != d:
         raise ValueError(f"stream on {stream.device}, tensors on cuda:{d}")
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -438,7 +442,7 @@ def grouped_matmul(a: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Ten
     _expect(y, (rows, N), odt, "y")
     d = _device(a, w, offsets, row_weight, y, ws)
     if _elsewhere(d, stream):
-        with _on(d, stream):
+        with _on(d, stream, a, w, offsets, row_weight, y, ws):
             return grouped_matmul(a, w, offsets, transposed, row_weight, y, out, ws)
     if y is None:
         y = a.new_empty(rows, N, dtype=odt)
@@ -468,7 +472,7 @@ def grouped_wgrad(dy: torch.Tensor, a: torch.Tensor, offsets: Optional[torch.Ten
     _expect(dw, (E, N, K), odt, "dw")
     d = _device(a, dy, offsets, dw, ws)
     if _elsewhere(d, stream):
-        with _on(d, stream):
+        with _on(d, stream, a, dy, offsets, dw, ws):
             return grouped_wgrad(dy, a, offsets, dw, accumulate, out, ws)
     if dw is None:
         dw = a.new_empty(E, N, K, dtype=odt)
@@ -500,7 +504,7 @@ def grouped_matmul_nvfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     _expect(y, (rows, N), odt, "y")
     d = _device(a, a_scales, w, w_scales, offsets, a_row_scale, w_row_scale, row_weight, y, ws)
     if _elsewhere(d, stream):
-        with _on(d, stream):
+        with _on(d, stream, a, a_scales, w, w_scales, offsets, a_row_scale, w_row_scale, row_weight, y, ws):
             return grouped_matmul_nvfp4(a, a_scales, w, w_scales, offsets, a_row_scale, w_row_scale, row_weight, y, out,
                                         ws)
     if y is None:
@@ -556,7 +560,7 @@ def quantize_nvfp4(x: torch.Tensor, row_token: Optional[torch.Tensor] = None, of
         _expect(row_token, (rows,), torch.int32, "row_token")
     d = _device(x, row_token, offsets, *(out.values() if out else ()))
     if _elsewhere(d, stream):
-        with _on(d, stream):
+        with _on(d, stream, x, row_token, offsets, *(out.values() if out else ())):
             return quantize_nvfp4(x, row_token, offsets, row_scaled, values, out)
     o = _nvfp4_outputs(rows, cols, x, row_scaled, values, out)
     _check(lib.moe_quantize_nvfp4(rows, cols, dt, x.data_ptr(), x_rows, _p(row_token), _live(offsets),
@@ -580,7 +584,7 @@ def swiglu_quantize_nvfp4(gu: torch.Tensor, clamp: float = 0.0, clamp_mode="prea
     rows, cols, dt = _gate_up(gu)
     d = _device(gu, offsets, *(out.values() if out else ()))
     if _elsewhere(d, stream):
-        with _on(d, stream):
+        with _on(d, stream, gu, offsets, *(out.values() if out else ())):
             return swiglu_quantize_nvfp4(gu, clamp, clamp_mode, offsets, row_scaled, values, out)
     o = _nvfp4_outputs(rows, cols, gu, row_scaled, values, out)
     _check(lib.moe_swiglu_quantize_nvfp4(rows, cols, dt, gu.data_ptr(), clamp, CLAMP_MODES[clamp_mode], _live(offsets),
@@ -596,7 +600,7 @@ def swiglu(gu: torch.Tensor, clamp: float = 0.0, clamp_mode="preact", offsets: O
     _expect(h, (rows, F), gu.dtype, "h")
     d = _device(gu, offsets, h)
     if _elsewhere(d, stream):
-        with _on(d, stream):
+        with _on(d, stream, gu, offsets, h):
             return swiglu(gu, clamp, clamp_mode, offsets, h)
     if h is None:
         h = gu.new_empty(rows, F)
@@ -624,7 +628,7 @@ def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, row_weight: Optional[tor
     _expect(drw, (rows,), torch.float32, "drow_weight")
     d = _device(gu, dh, row_weight, offsets, dgu, hw, drw)
     if _elsewhere(d, stream):
-        with _on(d, stream):
+        with _on(d, stream, gu, dh, row_weight, offsets, dgu, hw, drw):
             return swiglu_backward(gu, dh, row_weight, clamp, clamp_mode, offsets, need_hw, need_drow_weight, out)
     if dgu is None:
         dgu = torch.empty_like(gu)
