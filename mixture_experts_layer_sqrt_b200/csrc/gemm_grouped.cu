@@ -26,13 +26,15 @@
 //
 // Measured (B200, 1 kW limit; cool clocks / after a second of the same call):
 //   16 rows x 4096 x 28672 over 8 groups      284 us = 6.6 TB/s, a copy's rate
-//   15001 x 8192 x 2048 over 64 groups        498-520 / 633 us (DRAM 5 TB/s and
-//                                             0.97 PFLOP/s at once, 1.4 GHz)
-//   65536 x 4096 x 1536 over 128 (NN)         660 / 880 us, tensor pipe 90%
-//   8192 rows, dW 8 x 4096 x 14336 (TN)       700 / 820 us, tensor pipe 84%
-// All of the last three are held by the power limit: the clock falls to 1.2-1.4
-// GHz, and below after a while.  One cuBLAS product of the second's and third's
-// sizes (a single weight matrix): 388 and 557 us.
+//   15001 x 8192 x 2048 over 64 groups        504 / 610 us (cool: DRAM 5 TB/s and
+//                                             1 PFLOP/s at once, 1.4 GHz)
+//   65536 x 4096 x 1536 over 128 (NN)         661-810 / 883 us, tensor pipe 90%
+//   8192 rows, dW 8 x 4096 x 14336 (TN)       679 / 795 us, tensor pipe 85%
+// All of the last three are held by the power limit: the clock falls to 1.3-1.5
+// GHz, and to 980, 990 and 1290 MHz after a while.  One cuBLAS product of their sizes
+// (a single weight matrix) takes 338 / 398, 556 / 653 and 643 / 765 us.  Added to an
+// existing dW the last takes 4.1 ms in fp32 and 2.9 in bf16 (see the epilogue's loop
+// over the old values).
 //
 // A K-major tile lies in shared memory as rows of 64 reduction elements (128
 // bytes, 128-byte swizzle); an MN-major tile as boxes of 64 features x 64
@@ -731,8 +733,10 @@ moe_status launch_grouped_bf16(const MoEGrouped &g, const void *a, const int32_t
   p.out_f32 = g.out_dtype == MOE_F32;
   p.status = status;
   // few rows a group: single CTAs with narrow token tiles.  8 / 16 / 64 / 96 / 128
-  // rows in each of 32 groups x 4096 x 2048: 91 / 94 / 97 / 112 / 116 us so, with
-  // pairs 97 / 99 / 103 / 106 / 109.
+  // rows in each of 32 groups x 4096 x 2048: 91 / 92 / 96 / 112 / 114 us so, with
+  // pairs 96 / 97 / 102 / 104 / 106.  The host knows the average only: 8192 rows over
+  // 128 groups take 346 us so and 359 with pairs when equal, 407 and 368 with sizes
+  // as 1 / i.
   const bool narrow = g.rows <= 64l * g.groups;
   if (transposed) return narrow ? launch<NN, 64>(p, w, a, s) : launch<NN, 256>(p, w, a, s);
   return narrow ? launch<NT, 64>(p, w, a, s) : launch<NT, 256>(p, w, a, s);

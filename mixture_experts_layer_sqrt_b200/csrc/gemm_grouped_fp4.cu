@@ -9,8 +9,8 @@
 //
 // Layout of the work as in gemm_grouped.cu: weights on the MMA's M side (128
 // output features a tile), the tokens of one group on its N side (up to BT,
-// rounded to 16), so ragged groups pad nothing and the packed weights are read
-// once per BT tokens.  A stage of codes holds 256 reduction elements, rows of
+// rounded to 16), so ragged groups pad few columns and no rows, and the packed
+// weights are read once per BT tokens.  A stage of codes holds 256 reduction elements, rows of
 // 128 bytes (128-byte swizzle); a stage of scales those of four of them, rows of
 // 64 bytes (64-byte swizzle).  TMA's cost is by the row here: 49152 rows x 4096
 // x 2048 over 384 groups took 418-427 us with 16 bytes of scales a row and
@@ -29,8 +29,8 @@
 //
 // Measured (B200): 48 rows x 4096 x 2048 over 384 groups 46 us (227 MB of weights
 // at 4.9 TB/s; the last tiles, with five or six a CTA, and the start take the
-// rest); 49152 rows 386-400 us (2.1 GB, 5.4 TB/s), 471 us after a second under the
-// power limit; 8192 rows x 4096 x 4096 over 4 groups 88 us = 3.1 PFLOP/s.
+// rest); 49152 rows 383-407 us (2.1 GB, 5.4 TB/s), 464 us after a second under the
+// power limit; 8192 rows x 4096 x 4096 over 4 groups 89 us = 3.1 PFLOP/s.
 #include <cudaTypedefs.h>
 #include <limits.h>
 
@@ -617,8 +617,9 @@ moe_status launch_grouped_nvfp4(const MoEGrouped &g, const void *a, const void *
   p.out_f32 = g.out_dtype == MOE_F32;
   p.status = status;
   // 64-token tiles and a deeper weight ring for few rows a group: 8 / 16 / 64 / 96
-  // rows in each of 32 groups x 4096 x 2048: 35 / 35 / 38 / 50 us so, with tiles of
-  // up to 192 tokens 38 / 37 / 40 / 42
+  // rows in each of 32 groups x 4096 x 2048: 35 / 35 / 39 / 50 us so, with tiles of
+  // up to 192 tokens 37 / 37 / 39 / 41.  8192 rows over 128 groups: 113 us so and 119
+  // with 192 when equal, 145 and 128 with sizes as 1 / i.
   const bool narrow = g.rows <= 64l * g.groups;
   const bool sf_tma = g.k % 256 == 0;
   if (narrow) return sf_tma ? launch<64, true>(p, a, w, s) : launch<64, false>(p, a, w, s);

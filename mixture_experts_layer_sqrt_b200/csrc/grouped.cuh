@@ -48,10 +48,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *a
 }
 
 // True in one lane of a converged warp, the same one every time.  The
-// producer and the MMA issuer run their whole loops under it: known to be one
-// thread, the compiler keeps the operands of copies and MMAs in uniform
-// registers and issues them without a vote.  With the state of the next stage's
-// barrier read ahead of the MMAs (peek), an issue loop of 4 MMAs a stage takes
+// producer and the MMA issuer run their whole loops under it.  With the state of the
+// next stage's barrier read ahead of the MMAs, an issue loop of 4 MMAs a stage takes
 // 245 cycles, against 395 with a vote, an election and a wait per stage and 650
 // under `lane == 0`; 4 MMAs of N = 128 take 256 cycles, of N = 256 512 (one CTA
 // an SM, nothing to wait for).

@@ -26,9 +26,10 @@
 // the row maximum and the codes; longer rows are read twice (from L2).  With few
 // rows four warps share one whatever its length.
 //
-// Measured (B200): 49152 rows x 4096 gathered from 8192, with the values, 119 us:
-// 513 MB written (a fill of as much takes 131 us); 16384 rows x 4096 from gate|up
-// 94 us (SwiGLU's accurate exponential and reciprocal beside 440 MB).
+// Measured (B200): 49152 rows x 4096 gathered from 8192, with the values, 118 us:
+// 513 MB written (a fill of as much takes 131 us), and 77 us without them; 16384 rows
+// x 4096 from gate|up 95 us, 108 with the clamp (SwiGLU's accurate exponential and
+// reciprocal beside 440 MB).
 #include <cuda_fp8.h>
 
 #include "act.cuh"
