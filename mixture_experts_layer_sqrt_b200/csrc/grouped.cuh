@@ -14,7 +14,7 @@ namespace grouped {
 constexpr int MAX_E = 1024;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr uint64_t kDrainLimitNs = 200000000ull;  // 0.2 s
-constexpr uint64_t kStepNs = 4000;                // a stage of a reduction takes 0.2-0.3 us, 1.5 with the SM's share of HBM
+constexpr uint64_t kStepNs = 4000;                // a stage of a reduction takes 0.2-0.3 us, under 1 when bound by HBM
 
 // Bounded wait; false if the CTA is aborting (this thread may have started
 // it).  `steps`: stages of a reduction that pass meanwhile, for the waits that span
