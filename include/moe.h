@@ -353,7 +353,10 @@ moe_status moe_grouped_wgrad(const MoEGrouped *g, const void *dy, const void *a,
  *   a uint8 [rows, k/2], a_scales [rows, k/16], a_row_scale [rows] or NULL (= 1)
  *   w uint8 [E, n, k/2], w_scales [E, n, k/16], w_row_scale [E, n] or NULL
  *   row_weight [rows] or NULL; y [rows, n] out_dtype; g->dtype = MOE_NVFP4
- * Codes times scales are multiplied exactly and accumulated in fp32. */
+ * Codes times scales are multiplied exactly and accumulated in fp32.  A scale is a
+ * magnitude here: its sign bit, which no quantiser sets, is not read (the expert
+ * stages and their NVFP4 weights take it as e4m3's).  A NaN scale (0x7f) makes its
+ * token's row, or its feature's column of the group, NaN. */
 moe_status moe_grouped_matmul_nvfp4(const MoEGrouped *g, const void *a, const void *a_scales, const float *a_row_scale,
                                     const int32_t *expert_offsets, const void *w, const void *w_scales,
                                     const float *w_row_scale, const float *row_weight, void *y, void *ws,

@@ -486,7 +486,8 @@ def grouped_matmul_nvfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
                          offsets: Optional[torch.Tensor], a_row_scale=None, w_row_scale=None, row_weight=None, y=None,
                          out: Optional[str] = None, ws=None, stream=None) -> torch.Tensor:
     """Rows of group e times w[e]^T, both NVFP4: a uint8 [rows, K/2] with a_scales [rows, K/16],
-    w uint8 [E, N, K/2] with w_scales [E, N, K/16], optional fp32 row scales of either."""
+    w uint8 [E, N, K/2] with w_scales [E, N, K/16], optional fp32 row scales of either.  The scales
+    are magnitudes: their sign bit is not read."""
     _matrix(a, 2, "a")
     _matrix(w, 3, "w")
     rows, K = a.shape[0], 2 * a.shape[1]
