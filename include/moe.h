@@ -21,7 +21,8 @@
  *  - Pointers named in the argument lists are DEVICE pointers owned by the
  *    caller, unless documented as host.  The library allocates and frees no
  *    memory; scratch comes from the caller's workspace `ws`.
- *  - Tensors are dense row-major (last index fastest), 16-byte aligned.
+ *  - Tensors are dense row-major (last index fastest), 16-byte aligned.  An
+ *    output shares no memory with an input, unless its comment allows it.
  *  - Every call is asynchronous on `stream` (a cudaStream_t; NULL = legacy
  *    default stream).  Argument errors are detected on the host and returned
  *    synchronously, before anything is enqueued.  Device-side errors (a
